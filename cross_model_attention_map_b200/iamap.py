@@ -106,6 +106,18 @@ _SIGS = {
                                   _I64, _P, _SZ, _P]),
     "iamap_mapped_av_chunk": (_I, [_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I, _I, _P, _P, _P,
                                    _P, _P, _I64, _P, _I, _I, _P, _I, _P, _P, _SZ, _P]),
+    "iamap_cache_write": (_I, [_P, _I64, _I64, _P, _P, _I, _P, _I, _I, _I64, _I, _I, _I, _P, _P,
+                               _P]),
+    "iamap_cache_read": (_I, [_P, _P, _I64, _P, _I, _I, _P, _P, _I, _I64, _I, _I, _I, _P, _P]),
+    "iamap_sender_rows_quant_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "iamap_sender_rows_quant": (_I, [_P, _P, _P, _I64, _P, _I, _I, _P, _I, _I, _I, _I, _I, _I, _P,
+                                     _I, _P, _SZ, _P]),
+    "iamap_mapped_av_paged_quant_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "iamap_mapped_av_paged_quant": (_I, [_P, _I, _P, _P, _P, _I64, _P, _I, _I, _P, _I, _I, _I, _I,
+                                         _I, _I, _I, _P, _P, _SZ, _P]),
+    "iamap_attention_paged_quant_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "iamap_attention_paged_quant": (_I, [_P, _P, _P, _I, _P, _P, _I, _I64, _P, _I, _I, _P, _I, _I,
+                                         _I, _I, _I, _P, _P, _P, _SZ, _P]),
 }
 
 EXPORTED = tuple(_SIGS)
@@ -514,6 +526,59 @@ def iamap_prefix_lookup(keys, count, key_cu, num_seqs, table_keys, table_vals, c
         _ptr(found), _ptr(hit_blocks), _stream(stream)))
 
 
+def iamap_cache_write(x, x_stride, n, cu, starts, num_seqs, page_table, max_pages, page_size,
+                      num_pages, H, d, bits, codes, scales, stream=None):
+    _check("iamap_cache_write", _lib.iamap_cache_write(
+        _ptr(x), x_stride, n, _ptr(cu), _ptr(starts), num_seqs, _ptr(page_table), max_pages,
+        page_size, num_pages, H, d, bits, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def iamap_cache_read(codes, scales, num_pages, page_table, max_pages, page_size, cu, starts,
+                     num_seqs, n, H, d, bits, out, stream=None):
+    _check("iamap_cache_read", _lib.iamap_cache_read(
+        _ptr(codes), _ptr(scales), num_pages, _ptr(page_table), max_pages, page_size, _ptr(cu),
+        _ptr(starts), num_seqs, n, H, d, bits, _ptr(out), _stream(stream)))
+
+
+def iamap_sender_rows_quant_workspace_bytes(batch, H_s, max_ctx) -> int:
+    return _lib.iamap_sender_rows_quant_workspace_bytes(batch, H_s, max_ctx)
+
+
+def iamap_sender_rows_quant(q, k_codes, k_scales, num_pages, page_table, max_pages, page_size,
+                            ctx_lens, max_ctx, batch, H_s, H_k, d, bits, p_rows, ctx_stride, ws,
+                            stream=None):
+    _check("iamap_sender_rows_quant", _lib.iamap_sender_rows_quant(
+        _ptr(q), _ptr(k_codes), _ptr(k_scales), num_pages, _ptr(page_table), max_pages, page_size,
+        _ptr(ctx_lens), max_ctx, batch, H_s, H_k, d, bits, _ptr(p_rows), ctx_stride, _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def iamap_mapped_av_paged_quant_workspace_bytes(batch, H_r, d_v, max_ctx) -> int:
+    return _lib.iamap_mapped_av_paged_quant_workspace_bytes(batch, H_r, d_v, max_ctx)
+
+
+def iamap_mapped_av_paged_quant(p_rows, ctx_stride, W, v_codes, v_scales, num_pages, page_table,
+                                max_pages, page_size, ctx_lens, max_ctx, batch, H_s, H_r, H_kv,
+                                d_v, bits, out, ws, stream=None):
+    _check("iamap_mapped_av_paged_quant", _lib.iamap_mapped_av_paged_quant(
+        _ptr(p_rows), ctx_stride, _ptr(W), _ptr(v_codes), _ptr(v_scales), num_pages,
+        _ptr(page_table), max_pages, page_size, _ptr(ctx_lens), max_ctx, batch, H_s, H_r, H_kv,
+        d_v, bits, _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def iamap_attention_paged_quant_workspace_bytes(batch, H_q, d, max_ctx) -> int:
+    return _lib.iamap_attention_paged_quant_workspace_bytes(batch, H_q, d, max_ctx)
+
+
+def iamap_attention_paged_quant(q, k_codes, k_scales, k_bits, v_codes, v_scales, v_bits, num_pages,
+                                page_table, max_pages, page_size, ctx_lens, max_ctx, batch, H_q,
+                                H_kv, d, out, lse, ws, stream=None):
+    _check("iamap_attention_paged_quant", _lib.iamap_attention_paged_quant(
+        _ptr(q), _ptr(k_codes), _ptr(k_scales), k_bits, _ptr(v_codes), _ptr(v_scales), v_bits,
+        num_pages, _ptr(page_table), max_pages, page_size, _ptr(ctx_lens), max_ctx, batch, H_q,
+        H_kv, d, _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
 # ------------------------------------------------------------------------------------------------
 # Buffer helpers (torch allocations in the documented shapes)
 # ------------------------------------------------------------------------------------------------
@@ -531,6 +596,14 @@ def alloc_compress_outputs(n, H_s, num_rowblocks, num_causal_blocks, device="cud
         val_off=torch.empty(max(num_causal_blocks, 1), dtype=i64, device=device),
         counts=torch.zeros(2, dtype=i64, device=device),
     )
+
+
+def alloc_quant_cache(num_pages, page_size, H, d, bits, device="cuda"):
+    """(codes, scales) of an empty quantised cache: every value reads back as 0."""
+    codes = torch.full((num_pages, H, page_size, d * bits // 8), 0x88 if bits == 4 else 0x80,
+                       dtype=torch.uint8, device=device)
+    scales = torch.zeros(num_pages, H, page_size, d // 32, dtype=torch.float16, device=device)
+    return codes, scales
 
 
 def alloc_workspace(nbytes, device="cuda"):

@@ -178,6 +178,180 @@ class DecodeStep:
         return self.out
 
 
+def _expect(name, t, dtype, shape, device):
+    """A tensor that the library will read through its address alone: right type, shape, device,
+    and packed."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, got %s %s on %s" % (
+            name, dtype, shape, device, t.dtype, tuple(t.shape), t.device))
+
+
+class QuantCache:
+    """A paged cache of keys or values held in 8 or 4 bits: `num_pages` pages of `page_size` tokens,
+    H heads of d elements (groups of 32 with one fp16 scale each; include/iamap.h states the
+    format). ``over`` makes one of buffers that the caller already has.
+
+        write(x, cu, starts, page_table)       new rows of packed sequences into their pages
+        read(cu, starts, page_table, out)      ranges of sequences as packed bf16 rows
+    """
+
+    def __init__(self, num_pages, page_size, H, d, bits, device="cuda"):
+        if bits not in (4, 8):
+            raise ValueError("a cache holds 4 or 8 bits an element")
+        if d not in (64, 128):
+            raise ValueError("head dim must be 64 or 128")
+        self._own(*C.alloc_quant_cache(num_pages, page_size, H, d, bits, device), bits)
+
+    @classmethod
+    def over(cls, codes, scales, bits):
+        """The cache whose buffers are `codes` uint8 [num_pages, H, page_size, d * bits / 8] and
+        `scales` fp16 [num_pages, H, page_size, d / 32]."""
+        self = cls.__new__(cls)
+        self._own(codes, scales, bits)
+        return self
+
+    def _own(self, codes, scales, bits):
+        if codes.dim() != 4 or bits not in (4, 8):
+            raise ValueError("codes [num_pages, H, page_size, d * bits / 8] in 4 or 8 bits expected")
+        self.num_pages, self.H, self.page_size = (int(x) for x in codes.shape[:3])
+        self.d, self.bits = int(codes.shape[3]) * 8 // bits, bits
+        self.device = codes.device
+        _expect("codes", codes, torch.uint8, tuple(codes.shape), self.device)
+        _expect("scales", scales, torch.float16,
+                (self.num_pages, self.H, self.page_size, self.d // 32), self.device)
+        self.codes, self.scales = codes, scales
+
+    def _ranges(self, cu, starts, page_table):
+        num_seqs = starts.numel()
+        _expect("cu", cu, torch.int32, (num_seqs + 1,), self.device)
+        _expect("starts", starts, torch.int32, (num_seqs,), self.device)
+        self._table(page_table, num_seqs)
+        return num_seqs
+
+    def _table(self, page_table, num_seqs):
+        if self.device.index != torch.cuda.current_device():
+            raise ValueError("the cache lies on %s, which is not the current device" % self.device)
+        _expect("page_table", page_table, torch.int32, (num_seqs, page_table.shape[-1]),
+                self.device)
+
+    def write(self, x, cu, starts, page_table, stream=None):
+        """Quantises row cu[s] + i of x as token starts[s] + i of sequence s. x: bf16 [n, H, d] or
+        [n, H * d]; its rows may lie further apart than H * d (a slice of a fused projection).
+        cu int32 [num_seqs + 1], starts int32 [num_seqs] and page_table int32
+        [num_seqs, max_pages] on the device."""
+        num_seqs = self._ranges(cu, starts, page_table)
+        n, width = int(x.shape[0]), self.H * self.d
+        rows = ((width,), (1,)) if x.dim() == 2 else ((self.H, self.d), (self.d, 1))
+        if (x.dtype != torch.bfloat16 or x.device != self.device
+                or tuple(x.shape[1:]) != rows[0] or (n and x.stride()[1:] != rows[1])):
+            raise ValueError("x must be bf16 [n, H, d] or [n, H * d] on %s with packed rows"
+                             % self.device)
+        C.iamap_cache_write(x, x.stride(0) if n > 1 else width, n, cu, starts, num_seqs,
+                            page_table, page_table.shape[1], self.page_size, self.num_pages,
+                            self.H, self.d, self.bits, self.codes, self.scales, stream)
+
+    def read(self, cu, starts, page_table, out, stream=None):
+        """Fills row cu[s] + i of out (bf16 [n, H, d]) with token starts[s] + i of sequence s and
+        returns out; rows behind the last sequence stay as they are."""
+        num_seqs = self._ranges(cu, starts, page_table)
+        n = int(out.shape[0])
+        _expect("out", out, torch.bfloat16, (n, self.H, self.d), self.device)
+        C.iamap_cache_read(self.codes, self.scales, self.num_pages, page_table,
+                           page_table.shape[1], self.page_size, cu, starts, num_seqs, n, self.H,
+                           self.d, self.bits, out, stream)
+        return out
+
+
+class QuantSenderRows:
+    """Buffers of the small model's attention rows over a quantised key cache (H_k key heads,
+    grouped if fewer than H_s): run(q, cache, page_table, ctx_lens) -> rows
+    [batch, H_s, ctx_stride], the p_rows of a mapped decode step. ctx_lens stays on the device;
+    max_ctx bounds it."""
+
+    def __init__(self, batch, H_s, d, max_ctx, H_k=None, ctx_stride=None, device="cuda"):
+        self.batch, self.H_s, self.d, self.max_ctx = batch, H_s, d, int(max_ctx)
+        self.H_k = H_s if H_k is None else int(H_k)
+        self.ctx_stride = max(1, self.max_ctx) if ctx_stride is None else int(ctx_stride)
+        self.ws = C.alloc_workspace(
+            C.iamap_sender_rows_quant_workspace_bytes(batch, H_s, self.max_ctx), device)
+        self.rows = torch.empty(batch, H_s, self.ctx_stride, dtype=torch.float32, device=device)
+
+    def run(self, q, cache, page_table, ctx_lens, stream=None):
+        _expect("q", q, torch.bfloat16, (self.batch, self.H_s, self.d), self.rows.device)
+        _expect("ctx_lens", ctx_lens, torch.int32, (self.batch,), self.rows.device)
+        _same_cache(cache, self.H_k, self.d)
+        cache._table(page_table, self.batch)
+        C.iamap_sender_rows_quant(q, cache.codes, cache.scales, cache.num_pages, page_table,
+                                  page_table.shape[1], cache.page_size, ctx_lens, self.max_ctx,
+                                  self.batch, self.H_s, self.H_k, self.d, cache.bits, self.rows,
+                                  self.ctx_stride, self.ws, stream)
+        return self.rows
+
+
+class QuantDecodeStep:
+    """Buffers of one decode step on a mapped layer over a quantised value cache:
+    run(p_rows, W, cache, page_table, ctx_lens) -> out [batch, H_r, d_v]."""
+
+    def __init__(self, batch, H_s, H_r, d_v, max_ctx, H_kv=None, ctx_stride=None, device="cuda"):
+        self.batch, self.H_s, self.H_r, self.d_v = batch, H_s, H_r, d_v
+        self.max_ctx = int(max_ctx)
+        self.H_kv = H_r if H_kv is None else int(H_kv)
+        self.ctx_stride = max(1, self.max_ctx) if ctx_stride is None else int(ctx_stride)
+        self.ws = C.alloc_workspace(
+            C.iamap_mapped_av_paged_quant_workspace_bytes(batch, H_r, d_v, self.max_ctx), device)
+        self.out = torch.empty(batch, H_r, d_v, dtype=torch.float32, device=device)
+
+    def run(self, p_rows, W, cache, page_table, ctx_lens, stream=None):
+        dev = self.out.device
+        _expect("p_rows", p_rows, torch.float32, (self.batch, self.H_s, self.ctx_stride), dev)
+        _expect("W", W, torch.float32, (self.H_r, self.H_s), dev)
+        _expect("ctx_lens", ctx_lens, torch.int32, (self.batch,), dev)
+        _same_cache(cache, self.H_kv, self.d_v)
+        cache._table(page_table, self.batch)
+        C.iamap_mapped_av_paged_quant(p_rows, self.ctx_stride, W, cache.codes, cache.scales,
+                                      cache.num_pages, page_table, page_table.shape[1],
+                                      cache.page_size, ctx_lens, self.max_ctx, self.batch,
+                                      self.H_s, self.H_r, self.H_kv, self.d_v, cache.bits,
+                                      self.out, self.ws, stream)
+        return self.out
+
+
+class QuantAttention:
+    """Buffers of one decode attention over quantised keys and values (a layer that is not mapped,
+    or the small model's own): run(q, k_cache, v_cache, page_table, ctx_lens) -> out bf16
+    [batch, H_q, d], or (out, lse fp32 [batch, H_q]) with want_lse."""
+
+    def __init__(self, batch, H_q, d, max_ctx, H_kv=None, want_lse=False, device="cuda"):
+        self.batch, self.H_q, self.d, self.max_ctx = batch, H_q, d, int(max_ctx)
+        self.H_kv = H_q if H_kv is None else int(H_kv)
+        self.ws = C.alloc_workspace(
+            C.iamap_attention_paged_quant_workspace_bytes(batch, H_q, d, self.max_ctx), device)
+        self.out = torch.empty(batch, H_q, d, dtype=torch.bfloat16, device=device)
+        self.lse = torch.empty(batch, H_q, dtype=torch.float32, device=device) if want_lse else None
+
+    def run(self, q, k_cache, v_cache, page_table, ctx_lens, stream=None):
+        _expect("q", q, torch.bfloat16, (self.batch, self.H_q, self.d), self.out.device)
+        _expect("ctx_lens", ctx_lens, torch.int32, (self.batch,), self.out.device)
+        _same_cache(k_cache, self.H_kv, self.d)
+        _same_cache(v_cache, self.H_kv, self.d)
+        if (k_cache.num_pages, k_cache.page_size) != (v_cache.num_pages, v_cache.page_size):
+            raise ValueError("keys and values must share their pages")
+        k_cache._table(page_table, self.batch)
+        C.iamap_attention_paged_quant(q, k_cache.codes, k_cache.scales, k_cache.bits,
+                                      v_cache.codes, v_cache.scales, v_cache.bits,
+                                      k_cache.num_pages, page_table, page_table.shape[1],
+                                      k_cache.page_size, ctx_lens, self.max_ctx, self.batch,
+                                      self.H_q, self.H_kv, self.d, self.out, self.lse, self.ws,
+                                      stream)
+        return self.out if self.lse is None else (self.out, self.lse)
+
+
+def _same_cache(cache, H, d):
+    if cache.H != H or cache.d != d:
+        raise ValueError("a cache of %d heads of %d expected, got %d of %d" % (H, d, cache.H,
+                                                                              cache.d))
+
+
 class HeadMatch:
     """Buffers of one head-matching calibration."""
 

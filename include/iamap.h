@@ -35,6 +35,12 @@
  *                block of a prompt, insert of (key, location) pairs into a device hash table,
  *                lookup of a prompt's blocks and of its longest cached prefix. (MapFlow news
  *                page, storage-and-execution part, second component.)
+ *   quantised cache  a paged cache held in 8 or 4 bits: iamap_cache_write quantises new keys or
+ *                values into their pages, iamap_cache_read reads ranges of sequences back, and the
+ *                decode operators read it directly: iamap_sender_rows_quant,
+ *                iamap_mapped_av_paged_quant and, for the layers that are not mapped,
+ *                iamap_attention_paged_quant. (Decode is bound by the bytes of the cache; IAM's
+ *                mapped layers halve it, fewer bits an element shorten the rest.)
  *   iamap_selftest_wait_timeout  exercises the bounded-wait failure path on the GPU.
  *   iamap_selftest_exp2  evaluates the FMA-pipe exponential that the compress kernels can use
  *                beside the MUFU one, for accuracy tests.
@@ -565,6 +571,108 @@ int iamap_prefix_insert(const uint64_t* keys, const int64_t* values, int64_t cou
 int iamap_prefix_lookup(const uint64_t* keys, int64_t count, const int64_t* key_cu, int num_seqs,
                         const uint64_t* table_keys, const int64_t* table_vals, int64_t capacity,
                         int64_t* found, int32_t* hit_blocks, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Quantised paged cache: keys or values of decode held in 8 or 4 bits.
+ *
+ * A (token, head) row of d elements (d = 64 or 128) is d / 32 groups of 32. A group is stored as
+ * integer codes c in [-Q, Q] (bits = 4: Q = 7; bits = 8: Q = 127) and one fp16 scale s, and stands
+ * for the values c * s:
+ *     s = fp16(min(m / Q, 65504)), m = max |x| over the group (both roundings to nearest even)
+ *     c = clamp(rint(x / s), -Q, Q), ties to even; c = 0 where s = 0
+ *     a group holding an infinity or NaN: s = NaN, c = 0 (every value reads back as NaN)
+ * |x - c s| <= s / 2 for every x with m in [Q 2^-14, 65504 Q]. Below that range the scale is a
+ * subnormal fp16 number (values under about Q 2^-26 become 0), above it values saturate.
+ *   codes   uint8 [num_pages, H, page_size, d * bits / 8]   16-byte aligned
+ *   scales  fp16  [num_pages, H, page_size, d / 32]         16-byte aligned
+ * Token j of sequence b is slot j % page_size of page page_table[b * max_pages + j / page_size].
+ * In a row, element 32 g + 4 r + i (r < 8, i < 4) is code number r * (d / 8) + 4 g + i, stored with
+ * an offset: byte c + 128 (8 bits), or nibble c + 8, low nibble first (4 bits). Codes and scales
+ * of slots at or past a sequence's length are never used (they may hold anything).
+ *
+ * The decode calls read the lengths (ctx_lens) on the device only: max_ctx bounds them and sizes the
+ * launch, so a captured graph may be replayed with other lengths up to max_ctx. A length outside
+ * [0, max_ctx] is clamped and sets IAMAP_DEV_BAD_INDEX. A page index outside [0, num_pages) makes
+ * its tokens count as absent (probability or contribution 0) and sets IAMAP_DEV_BAD_INDEX.
+ * A workspace belongs to one call in flight: calls that may overlap on the GPU, captured graphs
+ * among them, need one each.
+ * ------------------------------------------------------------------------------------------- */
+
+/*
+ * Quantises new rows into their pages.
+ *   x       bf16, row i's head h at x + i * x_stride + h * d (x_stride in elements, a multiple of 8,
+ *           at least H * d: a slice of a fused projection's output needs no copy); 16-byte aligned
+ *   n       rows of x; row cu[s] + i of sequence s (device int32 cu [num_seqs + 1]) becomes token
+ *           starts[s] + i (device int32 [num_seqs]). Rows outside [cu[0], cu[num_seqs]) (a padded
+ *           batch) are ignored.
+ * A row whose token lies outside the page table, or whose page index is outside [0, num_pages), is
+ * not stored and sets IAMAP_DEV_BAD_INDEX. The slots that one call writes must be distinct (rows of
+ * two sequences must not share a slot). Only those slots' bytes change. Asynchronous on stream.
+ */
+int iamap_cache_write(const void* x, int64_t x_stride, int64_t n, const int32_t* cu,
+                      const int32_t* starts, int num_seqs, const int32_t* page_table, int max_pages,
+                      int page_size, int64_t num_pages, int H, int d, int bits, void* codes,
+                      void* scales, void* stream);
+
+/*
+ * Reads ranges of sequences back as packed rows, e.g. the keys [0, e_s) that iamap_compress_chunk
+ * takes: row cu[s] + i of out (bf16 [n, H, d], 16-byte aligned) is token starts[s] + i of sequence
+ * s, bf16(c * s). Rows outside [cu[0], cu[num_seqs]) are left as they are; a token outside the page
+ * table or on a bad page reads as 0 and sets IAMAP_DEV_BAD_INDEX. Asynchronous on stream.
+ */
+int iamap_cache_read(const void* codes, const void* scales, int64_t num_pages,
+                     const int32_t* page_table, int max_pages, int page_size, const int32_t* cu,
+                     const int32_t* starts, int num_seqs, int64_t n, int H, int d, int bits,
+                     void* out, void* stream);
+
+/*
+ * iamap_sender_rows over a quantised key cache, with grouped keys: p_rows[b, h, j] = softmax over
+ * j < ctx_lens[b] of q[b, h] . k[b, j, h / (H_s / H_k)] / sqrt(d).
+ *   q       bf16 [batch, H_s, d], 16-byte aligned; H_k key heads, H_k divides H_s
+ *   p_rows  fp32 [batch, H_s, ctx_stride], ctx_stride >= max_ctx, written in full (zeros at
+ *           j >= ctx_lens[b]; a sequence of length 0 has a row of zeros)
+ *   ws      iamap_sender_rows_quant_workspace_bytes bytes
+ * The result feeds iamap_mapped_av_paged_quant (or iamap_mapped_av_paged) as its p_rows.
+ */
+size_t iamap_sender_rows_quant_workspace_bytes(int batch, int H_s, int max_ctx);
+int iamap_sender_rows_quant(const void* q, const void* k_codes, const void* k_scales,
+                            int64_t num_pages, const int32_t* page_table, int max_pages,
+                            int page_size, const int32_t* ctx_lens, int max_ctx, int batch, int H_s,
+                            int H_k, int d, int bits, float* p_rows, int ctx_stride, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/*
+ * iamap_mapped_av_paged_gqa over a quantised value cache:
+ *   out[b, r, :] = sum_{j < ctx_lens[b]} (sum_s W[r, s] * p_rows[b, s, j]) * v[b, j, r / (H_r / H_kv), :]
+ * p_rows fp32 [batch, H_s, ctx_stride] (entries at j >= ctx_lens[b] are not used), W fp32
+ * [H_r, H_s], out fp32 [batch, H_r, d_v] (16-byte aligned). H_s, H_r <= 128; H_kv divides H_r.
+ * ws: iamap_mapped_av_paged_quant_workspace_bytes bytes.
+ */
+size_t iamap_mapped_av_paged_quant_workspace_bytes(int batch, int H_r, int d_v, int max_ctx);
+int iamap_mapped_av_paged_quant(const float* p_rows, int ctx_stride, const float* W,
+                                const void* v_codes, const void* v_scales, int64_t num_pages,
+                                const int32_t* page_table, int max_pages, int page_size,
+                                const int32_t* ctx_lens, int max_ctx, int batch, int H_s, int H_r,
+                                int H_kv, int d_v, int bits, float* out, void* ws, size_t ws_bytes,
+                                void* stream);
+
+/*
+ * Decode attention of an unmapped layer (or of the sender itself) over quantised pages, one query
+ * row a sequence: out[b, h] = sum_j p_j v[b, j, h / (H_q / H_kv)], p = softmax over
+ * j < ctx_lens[b] of q[b, h] . k[b, j, h / (H_q / H_kv)] / sqrt(d).
+ *   q, out  bf16 [batch, H_q, d], 16-byte aligned. out is rounded once, from fp32 sums.
+ *   lse     fp32 [batch, H_q] natural-log sum of exp(scaled logits), or NULL
+ * Keys and values lie in two pools with the same pages and page table, in k_bits and v_bits each.
+ * A sequence of length 0 has out 0 and lse -inf. H_kv divides H_q.
+ * ws: iamap_attention_paged_quant_workspace_bytes bytes.
+ */
+size_t iamap_attention_paged_quant_workspace_bytes(int batch, int H_q, int d, int max_ctx);
+int iamap_attention_paged_quant(const void* q, const void* k_codes, const void* k_scales, int k_bits,
+                                const void* v_codes, const void* v_scales, int v_bits,
+                                int64_t num_pages, const int32_t* page_table, int max_pages,
+                                int page_size, const int32_t* ctx_lens, int max_ctx, int batch,
+                                int H_q, int H_kv, int d, void* out, float* lse, void* ws,
+                                size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
