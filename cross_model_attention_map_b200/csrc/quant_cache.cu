@@ -159,6 +159,9 @@ int check_quant_pages(const void* codes, const void* scales, int64_t num_pages,
     return set_error(IAMAP_ERR_INVALID_ARG, "bad sizes of the cache");
   if (((reinterpret_cast<uintptr_t>(codes) | reinterpret_cast<uintptr_t>(scales)) & 15u) != 0)
     return set_error(IAMAP_ERR_INVALID_ARG, "codes and scales must be 16-byte aligned");
+  // the kernels number the (page, head, slot) rows in 32 bits
+  if (num_pages > 0 && (int64_t)H * page_size > 0xffffffffll / num_pages)
+    return set_error(IAMAP_ERR_UNSUPPORTED, "num_pages * H * page_size must be below 2^32");
   return IAMAP_OK;
 }
 
@@ -168,6 +171,7 @@ int check_quant_batch(const int32_t* ctx_lens, int max_ctx, int batch, int max_p
   if (batch < 1 || max_ctx < 0) return set_error(IAMAP_ERR_INVALID_ARG, "bad sizes");
   if ((int64_t)max_ctx > (int64_t)max_pages * page_size)
     return set_error(IAMAP_ERR_INVALID_ARG, "max_ctx=%d exceeds the page table", max_ctx);
+  if (max_ctx > 1 << 30) return set_error(IAMAP_ERR_UNSUPPORTED, "max_ctx must be at most 2^30");
   return IAMAP_OK;
 }
 

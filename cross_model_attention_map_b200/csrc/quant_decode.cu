@@ -263,54 +263,3 @@ extern "C" int iamap_mapped_av_paged_quant(const float* p_rows, int ctx_stride, 
   IAMAP_LAUNCH_CHECK("quant_mapped_kernel");
   return IAMAP_OK;
 }
-
-extern "C" size_t iamap_attention_paged_quant_workspace_bytes(int batch, int H_q, int d,
-                                                              int max_ctx) {
-  if (batch < 1 || H_q < 1 || d < 1 || max_ctx < 0) return 0;
-  return 256;
-}
-
-extern "C" int iamap_attention_paged_quant(const void* q, const void* k_codes, const void* k_scales,
-                                           int k_bits, const void* v_codes, const void* v_scales,
-                                           int v_bits, int64_t num_pages, const int32_t* page_table,
-                                           int max_pages, int page_size, const int32_t* ctx_lens,
-                                           int max_ctx, int batch, int H_q, int H_kv, int d,
-                                           void* out, float* lse, void* ws, size_t ws_bytes,
-                                           void* stream) {
-  clear_error();
-  int rc = check_quant_pages(k_codes, k_scales, num_pages, page_table, max_pages, page_size, H_kv, d,
-                             k_bits);
-  if (rc) return rc;
-  rc = check_quant_pages(v_codes, v_scales, num_pages, page_table, max_pages, page_size, H_kv, d,
-                         v_bits);
-  if (rc) return rc;
-  rc = check_quant_batch(ctx_lens, max_ctx, batch, max_pages, page_size);
-  if (rc) return rc;
-  if (H_q < 1 || H_q % H_kv != 0)
-    return set_error(IAMAP_ERR_INVALID_ARG, "H_kv=%d must divide H_q=%d", H_kv, H_q);
-  if (!q || !out) return set_error(IAMAP_ERR_INVALID_ARG, "null pointer");
-  if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15u) != 0)
-    return set_error(IAMAP_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
-  const size_t need = iamap_attention_paged_quant_workspace_bytes(batch, H_q, d, max_ctx);
-  if (!ws || ws_bytes < need)
-    return set_error(IAMAP_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws_bytes);
-  DeviceContext* ctx = device_context();
-  if (!ctx) return IAMAP_ERR_CUDA;
-  QuantDecodeParams p{};
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k = pages_of(k_codes, k_scales, num_pages, page_table, max_pages, page_size, H_kv);
-  p.v = pages_of(v_codes, v_scales, num_pages, page_table, max_pages, page_size, H_kv);
-  p.k_bits = k_bits;
-  p.v_bits = v_bits;
-  p.ctx_lens = ctx_lens;
-  p.max_ctx = max_ctx;
-  p.Hq = H_q;
-  p.d = d;
-  p.scale_log2 = kLog2e / sqrtf((float)d);
-  p.out_bf16 = static_cast<__nv_bfloat16*>(out);
-  p.lse = lse;
-  p.status = ctx->status;
-  quant_softmax_kernel<false><<<dim3(H_q, batch), kTile, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  IAMAP_LAUNCH_CHECK("quant_softmax_kernel");
-  return IAMAP_OK;
-}
