@@ -212,54 +212,3 @@ extern "C" int iamap_sender_rows_quant(const void* q, const void* k_codes, const
   IAMAP_LAUNCH_CHECK("quant_softmax_kernel");
   return IAMAP_OK;
 }
-
-extern "C" size_t iamap_mapped_av_paged_quant_workspace_bytes(int batch, int H_r, int d_v,
-                                                              int max_ctx) {
-  if (batch < 1 || H_r < 1 || d_v < 1 || max_ctx < 0) return 0;
-  return 256;
-}
-
-extern "C" int iamap_mapped_av_paged_quant(const float* p_rows, int ctx_stride, const float* W,
-                                           const void* v_codes, const void* v_scales,
-                                           int64_t num_pages, const int32_t* page_table,
-                                           int max_pages, int page_size, const int32_t* ctx_lens,
-                                           int max_ctx, int batch, int H_s, int H_r, int H_kv,
-                                           int d_v, int bits, float* out, void* ws,
-                                           size_t ws_bytes, void* stream) {
-  clear_error();
-  int rc = check_quant_pages(v_codes, v_scales, num_pages, page_table, max_pages, page_size, H_kv,
-                             d_v, bits);
-  if (rc) return rc;
-  rc = check_quant_batch(ctx_lens, max_ctx, batch, max_pages, page_size);
-  if (rc) return rc;
-  if (H_r < 1 || H_r % H_kv != 0)
-    return set_error(IAMAP_ERR_INVALID_ARG, "H_kv=%d must divide H_r=%d", H_kv, H_r);
-  if (!p_rows || !W || !out) return set_error(IAMAP_ERR_INVALID_ARG, "null pointer");
-  if (H_s < 1 || H_s > 128 || H_r > 128)
-    return set_error(IAMAP_ERR_UNSUPPORTED, "H_s and H_r must be in [1, 128]");
-  if ((reinterpret_cast<uintptr_t>(out) & 15u) != 0)
-    return set_error(IAMAP_ERR_INVALID_ARG, "out must be 16-byte aligned");
-  if (ctx_stride < 1 || ctx_stride < max_ctx)
-    return set_error(IAMAP_ERR_INVALID_ARG, "ctx_stride=%d is below max_ctx=%d", ctx_stride, max_ctx);
-  const size_t need = iamap_mapped_av_paged_quant_workspace_bytes(batch, H_r, d_v, max_ctx);
-  if (!ws || ws_bytes < need)
-    return set_error(IAMAP_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws_bytes);
-  DeviceContext* ctx = device_context();
-  if (!ctx) return IAMAP_ERR_CUDA;
-  QuantDecodeParams p{};
-  p.v = pages_of(v_codes, v_scales, num_pages, page_table, max_pages, page_size, H_kv);
-  p.v_bits = bits;
-  p.ctx_lens = ctx_lens;
-  p.max_ctx = max_ctx;
-  p.Hq = H_r;
-  p.d = d_v;
-  p.rows = const_cast<float*>(p_rows);
-  p.stride = ctx_stride;
-  p.W = W;
-  p.H_s = H_s;
-  p.out_f32 = out;
-  p.status = ctx->status;
-  quant_mapped_kernel<<<dim3(H_r, batch), kTile, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  IAMAP_LAUNCH_CHECK("quant_mapped_kernel");
-  return IAMAP_OK;
-}
