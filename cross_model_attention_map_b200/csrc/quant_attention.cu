@@ -106,42 +106,9 @@ __global__ void __launch_bounds__(kThreads, 4) quant_attention_kernel(const Attn
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue(i);
 
-  // the query operand: head gid, elements 8 tid .. 8 tid + 7 of every group, brought near 2^7 by a power
-  // of two per head so that bf16 values of any size are exact in fp16 (a part 2^-21 of the largest or
-  // less is rounded)
   uint32_t qf[NG][4];
   float fq[2];
-  {
-    uint4 raw[NG];
-    uint32_t m = 0;
-    const bool live = gid < nh;
-    const __nv_bfloat16* q = p.q + ((int64_t)b * p.Hq + h0 + (live ? gid : 0)) * D + 8 * tid;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      raw[g] = live ? *reinterpret_cast<const uint4*>(q + 32 * g) : make_uint4(0, 0, 0, 0);
-      const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-    }
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const int down = min(253, max(1, 261 - (int)(m >> 7)));        // exponent field of 2^-e
-    const float f = __uint_as_float((uint32_t)down << 23);
-    const float back = __uint_as_float((uint32_t)(254 - down) << 23) * p.scale_log2;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16) * f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        qf[g][i] = pack_f16(v[q_elem<KB>(i, 0)], v[q_elem<KB>(i, 1)]);
-    }
-    fq[0] = __shfl_sync(0xffffffffu, back, 8 * tid);
-    fq[1] = __shfl_sync(0xffffffffu, back, 8 * tid + 4);
-  }
+  load_query<D, KB>(p.q + ((int64_t)b * p.Hq + h0) * D, nh, p.scale_log2, qf, fq);
 
   float o[2 * NG][4];
 #pragma unroll

@@ -1,0 +1,257 @@
+// iamap_sender_rows_quant: the small model's attention rows over a quantised key cache.
+//
+//   p[b, h, j] = 2^(x_j - lse2),  x_j = q[b, h] . k^[b, j, h / group] log2(e) / sqrt(d),  j < ctx[b]
+//
+// Bound by the key bytes (36 a token and head of 64 in 4 bits) and the rows written (4 bytes a token
+// and query head). The first kernel streams the keys as quant_attention.cu does, writes x in place of p
+// and the (reference, sum) of each range of tokens; the second joins a row's ranges in their order and
+// normalises its tokens, which are still in L2.
+#include <algorithm>
+
+#include "internal.h"
+#include "quant_tile.cuh"
+
+namespace iamap {
+namespace {
+
+using namespace qt;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 4;
+constexpr int kHeads = 8;            // query heads a CTA
+constexpr float kNoRef = -3e38f;
+
+struct RowsParams {
+  const __nv_bfloat16* q;
+  QuantPages k;
+  const int32_t* ctx_lens;
+  int max_ctx, batch, Hq, group, htiles;
+  int chunk, splits;
+  float scale_log2;
+  float* rows;                       // [batch, Hq, stride]
+  int stride;
+  float2* ml;                        // [batch * Hq][splits]: (reference, sum of 2^(x - reference))
+  unsigned int* status;
+};
+
+template <int D, int BITS, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads, 6) quant_rows_kernel(const RowsParams p) {
+  constexpr int NG = D / 32, K = kTok * D * BITS / 8, kStage = K + kTok * NG * 2;
+  __shared__ __align__(128) uint8_t smem[kWarps * kStages * kStage];
+  __shared__ uint32_t masks[kWarps][kStages];
+  __shared__ float2 ml_s[kWarps][kHeads];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tid = lane & 3;
+  int u = blockIdx.x;
+  const int ht = u % p.htiles;
+  u /= p.htiles;
+  const int hk = u % p.k.H;
+  u /= p.k.H;
+  const int b = u % p.batch, split = u / p.batch;
+  const int ctx = quant_ctx(p.ctx_lens, b, p.max_ctx, p.status);
+  const int j0 = split * p.chunk, j1 = min(ctx, j0 + p.chunk);
+  if (j0 >= j1) return;
+  const int h0 = hk * p.group + ht * kHeads;
+  const int nh = min(kHeads, p.group - ht * kHeads);
+  const int ntiles = max(0, (j1 - j0 + kTok - 1) / kTok - warp + kWarps - 1) / kWarps;
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
+  TileRows<ALIGNED> src;
+  src.init(&p.k, b, hk, j0 + warp * kTok, kWarps * kTok, j1, p.status);
+  auto issue = [&](int i) {
+    if (i < ntiles) {
+      const int s = i % kStages;
+      const uint32_t row = src.rows(i);
+      load_codes<D, BITS, ALIGNED>(ring + s * kStage, p.k.codes, row);
+      if (lane < 16) load_scales<D>(ring + s * kStage + K, p.k.scales, row);
+      const uint32_t m = __ballot_sync(0xffffffffu, row != kNoRow) & 0xffffu;
+      if (lane == 0) masks[warp][s] = m;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  uint32_t qf[NG][4];
+  float fq[2];
+  load_query<D, BITS>(p.q + ((int64_t)b * p.Hq + h0) * D, nh, p.scale_log2, qf, fq);
+  // a reference near the maximum, moved when a score exceeds it by more than 64 (sums stay in fp32)
+  float ref[2] = {kNoRef, kNoRef}, l[2] = {0.f, 0.f};
+  const int t0 = (gid >> 1) + 4 * (gid & 1);
+  float* row0 = p.rows + ((int64_t)b * p.Hq + h0 + 2 * tid) * p.stride + j0 + warp * kTok + t0;
+
+  for (int i = 0; i < ntiles; ++i) {
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    const uint32_t st = ring + (i % kStages) * kStage;
+    const uint32_t mask = masks[warp][i % kStages];
+    float x[4];
+    tile_scores<D, BITS>(st, st + K, qf, x);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] *= fq[c & 1];
+    if (mask != 0xffffu) {
+      if (!((mask >> t0) & 1)) x[0] = x[1] = -INFINITY;
+      if (!((mask >> (t0 + 8)) & 1)) x[2] = x[3] = -INFINITY;
+    }
+    if (__any_sync(0xffffffffu, fmaxf(x[0], x[2]) > ref[0] + 64.f || fmaxf(x[1], x[3]) > ref[1] + 64.f)) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float m = fmaxf(x[c], x[c + 2]);
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        if (m > ref[c] + 64.f) {
+          l[c] *= ex2(ref[c] - m);
+          ref[c] = m;
+        }
+      }
+    }
+    l[0] += ex2(x[0] - ref[0]) + ex2(x[2] - ref[0]);
+    l[1] += ex2(x[1] - ref[1]) + ex2(x[3] - ref[1]);
+    const int at = i * kWarps * kTok, j = j0 + warp * kTok + at + t0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (2 * tid + c < nh) {
+        if (j < j1) row0[(int64_t)c * p.stride + at] = x[c];
+        if (j + 8 < j1) row0[(int64_t)c * p.stride + at + 8] = x[c + 2];
+      }
+    __syncwarp();
+    issue(i + kStages - 1);
+  }
+  cp_async_wait<0>();
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    l[c] += __shfl_xor_sync(0xffffffffu, l[c], 4);
+    l[c] += __shfl_xor_sync(0xffffffffu, l[c], 8);
+    l[c] += __shfl_xor_sync(0xffffffffu, l[c], 16);
+    if (gid == 0) ml_s[warp][2 * tid + c] = make_float2(ref[c], l[c]);
+  }
+  __syncthreads();
+  if (threadIdx.x < nh) {
+    float m = kNoRef, z = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml_s[w][threadIdx.x].x);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) z += ml_s[w][threadIdx.x].y * ex2(ml_s[w][threadIdx.x].x - m);
+    p.ml[((int64_t)b * p.Hq + h0 + threadIdx.x) * p.splits + split] = make_float2(m, z);
+  }
+}
+
+constexpr int kNormTokens = 2048;    // tokens a CTA of the second kernel
+__global__ void __launch_bounds__(256) quant_rows_norm_kernel(const RowsParams p, int parts) {
+  const int part = blockIdx.x % parts;
+  const int64_t r = blockIdx.x / parts;                    // row b * Hq + h
+  const int ctx = min(max(p.ctx_lens[r / p.Hq], 0), p.max_ctx);
+  const int n = (ctx + p.chunk - 1) / p.chunk;
+  const float2* ml = p.ml + r * p.splits;
+  __shared__ float lse_s;
+  if (threadIdx.x < 32) {
+    float m = kNoRef, z = 0.f;
+    for (int s = threadIdx.x; s < n; s += 32) m = fmaxf(m, ml[s].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int s = threadIdx.x; s < n; s += 32) z = fmaf(ml[s].y, ex2(ml[s].x - m), z);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    if (threadIdx.x == 0) lse_s = z == 0.f ? INFINITY : m + log2f(z);
+  }
+  __syncthreads();
+  const float lse = lse_s;
+  float* row = p.rows + r * p.stride;
+  const int end = min(p.stride, (part + 1) * kNormTokens);
+  for (int j = part * kNormTokens + threadIdx.x; j < end; j += 256)
+    row[j] = j < ctx && lse != INFINITY ? ex2(row[j] - lse) : 0.f;
+}
+
+void rows_split(int units, int max_ctx, int* chunk, int* splits) {
+  const int64_t total = (int64_t)units * max_ctx;
+  int64_t c = (total + 148 * 6 - 1) / (148 * 6);
+  c = (c + 63) / 64 * 64;
+  *chunk = (int)std::min<int64_t>(2048, std::max<int64_t>(64, c));
+  *splits = std::max(1, (max_ctx + *chunk - 1) / *chunk);
+}
+
+template <int D>
+int launch_d(const RowsParams& p, int bits, unsigned int blocks, cudaStream_t st) {
+  const bool al = p.k.page_size % kTok == 0;
+  if (bits == 4) {
+    if (al) quant_rows_kernel<D, 4, true><<<blocks, kThreads, 0, st>>>(p);
+    else quant_rows_kernel<D, 4, false><<<blocks, kThreads, 0, st>>>(p);
+  } else {
+    if (al) quant_rows_kernel<D, 8, true><<<blocks, kThreads, 0, st>>>(p);
+    else quant_rows_kernel<D, 8, false><<<blocks, kThreads, 0, st>>>(p);
+  }
+  IAMAP_LAUNCH_CHECK("quant_rows_kernel");
+  const int parts = (p.stride + kNormTokens - 1) / kNormTokens;
+  quant_rows_norm_kernel<<<(unsigned int)((int64_t)p.batch * p.Hq * parts), 256, 0, st>>>(p, parts);
+  IAMAP_LAUNCH_CHECK("quant_rows_norm_kernel");
+  return IAMAP_OK;
+}
+
+}  // namespace
+}  // namespace iamap
+
+using namespace iamap;
+
+extern "C" size_t iamap_sender_rows_quant_workspace_bytes(int batch, int H_s, int max_ctx) {
+  if (batch < 1 || H_s < 1 || max_ctx < 0) return 0;
+  // the most that any grouping of the H_s heads needs
+  size_t most = 256;
+  for (int group = 1; group <= H_s; ++group) {
+    if (H_s % group != 0) continue;
+    int chunk, splits;
+    rows_split(batch * (H_s / group) * ((group + kHeads - 1) / kHeads), max_ctx, &chunk, &splits);
+    most = std::max(most, sizeof(float2) * (size_t)batch * H_s * splits);
+  }
+  return most;
+}
+
+extern "C" int iamap_sender_rows_quant(const void* q, const void* k_codes, const void* k_scales,
+                                       int64_t num_pages, const int32_t* page_table, int max_pages,
+                                       int page_size, const int32_t* ctx_lens, int max_ctx,
+                                       int batch, int H_s, int H_k, int d, int bits, float* p_rows,
+                                       int ctx_stride, void* ws, size_t ws_bytes, void* stream) {
+  clear_error();
+  int rc = check_quant_pages(k_codes, k_scales, num_pages, page_table, max_pages, page_size, H_k, d,
+                             bits);
+  if (rc) return rc;
+  rc = check_quant_batch(ctx_lens, max_ctx, batch, max_pages, page_size);
+  if (rc) return rc;
+  if (H_s < 1 || H_s % H_k != 0)
+    return set_error(IAMAP_ERR_INVALID_ARG, "H_k=%d must divide H_s=%d", H_k, H_s);
+  if (!q || !p_rows) return set_error(IAMAP_ERR_INVALID_ARG, "null pointer");
+  if ((reinterpret_cast<uintptr_t>(q) & 15u) != 0)
+    return set_error(IAMAP_ERR_INVALID_ARG, "q must be 16-byte aligned");
+  if (ctx_stride < 1 || ctx_stride < max_ctx)
+    return set_error(IAMAP_ERR_INVALID_ARG, "ctx_stride=%d is below max_ctx=%d", ctx_stride, max_ctx);
+  RowsParams p{};
+  p.group = H_s / H_k;
+  p.htiles = (p.group + kHeads - 1) / kHeads;
+  const int64_t units = (int64_t)batch * H_k * p.htiles;
+  if (units > 0x7fffff ||
+      (int64_t)batch * H_s * ((ctx_stride + (int64_t)kNormTokens - 1) / kNormTokens) > 0x7fffffff)
+    return set_error(IAMAP_ERR_UNSUPPORTED, "batch times heads times ctx_stride is too large");
+  rows_split((int)units, max_ctx, &p.chunk, &p.splits);
+  if (units * p.splits > 0x7fffffff)
+    return set_error(IAMAP_ERR_UNSUPPORTED, "batch times heads times max_ctx is too large");
+  const size_t need = sizeof(float2) * (size_t)batch * H_s * p.splits;
+  if (!ws || ws_bytes < need)
+    return set_error(IAMAP_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws_bytes);
+  if ((reinterpret_cast<uintptr_t>(ws) & 15u) != 0)
+    return set_error(IAMAP_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  DeviceContext* ctx = device_context();
+  if (!ctx) return IAMAP_ERR_CUDA;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = QuantPages{static_cast<const uint8_t*>(k_codes), static_cast<const __half*>(k_scales),
+                   num_pages, page_table, max_pages, page_size, H_k};
+  p.ctx_lens = ctx_lens;
+  p.max_ctx = max_ctx;
+  p.batch = batch;
+  p.Hq = H_s;
+  p.scale_log2 = kLog2e / sqrtf((float)d);
+  p.rows = p_rows;
+  p.stride = ctx_stride;
+  p.ml = static_cast<float2*>(ws);
+  p.status = ctx->status;
+  const unsigned int blocks = (unsigned int)(units * p.splits);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return d == 64 ? launch_d<64>(p, bits, blocks, st) : launch_d<128>(p, bits, blocks, st);
+}

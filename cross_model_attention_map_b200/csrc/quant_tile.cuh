@@ -144,6 +144,45 @@ __device__ __forceinline__ int q_elem(int p, int e) {
   return BITS == 4 ? p + 4 * e : 2 * p + e;
 }
 
+// The query operand of up to eight heads q[h * D], h < nh (the other columns are zero): head gid,
+// elements 8 tid .. 8 tid + 7 of every group. A head is brought near 2^7 by a power of two, so that bf16
+// values of any size are exact in fp16 (what is 2^-21 of the largest or less is rounded); fq[c] takes the
+// scores of columns 2 tid + c back, times `scale`.
+template <int D, int BITS>
+__device__ __forceinline__ void load_query(const __nv_bfloat16* q, int nh, float scale,
+                                           uint32_t (*qf)[4], float* fq) {
+  constexpr int NG = D / 32;
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  const bool live = gid < nh;
+  uint4 raw[NG];
+  uint32_t m = 0;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    raw[g] = live ? *reinterpret_cast<const uint4*>(q + gid * D + 32 * g + 8 * tid)
+                  : make_uint4(0, 0, 0, 0);
+    const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+  }
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const int down = min(253, max(1, 261 - (int)(m >> 7)));          // exponent field of the power of two
+  const float f = __uint_as_float((uint32_t)down << 23);
+  const float back = __uint_as_float((uint32_t)(254 - down) << 23) * scale;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16) * f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) qf[g][i] = pack_f16(v[q_elem<BITS>(i, 0)], v[q_elem<BITS>(i, 1)]);
+  }
+  fq[0] = __shfl_sync(0xffffffffu, back, 8 * tid);
+  fq[1] = __shfl_sync(0xffffffffu, back, 8 * tid + 4);
+}
+
 // Scores of a tile: s[0..1] = row gid, s[2..3] = row gid + 8, columns 2 tid and 2 tid + 1, in the
 // units of the fp16 query operand qf[group][4]. `codes` and `scales` are the tile's addresses.
 template <int D, int BITS>
