@@ -88,18 +88,19 @@ __global__ void __launch_bounds__(kThreads, 4) quant_attention_kernel(const Attn
   const uint32_t ring = smem_u32(smem) + warp * RB::kWarp;
   TileRows<ALIGNED> src;
   src.init(&p.k, b, hk, j0 + warp * kTok, kWarps * kTok, j1, p.status);
+  const uint8_t* kc = codes_base<D, KB, ALIGNED>(p.k.codes);
+  const uint8_t* vc = codes_base<D, VB, ALIGNED>(p.v_codes);
+  const __half* sc_pool = lane < 16 ? p.k.scales : p.v_scales;   // lanes 0..15 the keys' scales
+  const uint32_t sc_dst = lane < 16 ? RB::K : RB::K + RB::S + RB::V;
   auto issue = [&](int i) {
     if (i < ntiles) {
       const int s = i % kStages;
       const uint32_t dst = ring + s * RB::kStage;
-      const uint32_t row = src.rows(i);
-      load_codes<D, KB, ALIGNED>(dst, p.k.codes, row);
-      load_codes<D, VB, ALIGNED>(dst + RB::K + RB::S, p.v_codes, row);
-      // lanes 0..15 the keys' scales, 16..31 the values'
-      load_scales<D>(lane < 16 ? dst + RB::K : dst + RB::K + RB::S + RB::V,
-                     lane < 16 ? p.k.scales : p.v_scales, row);
-      const uint32_t m = __ballot_sync(0xffffffffu, row != kNoRow) & 0xffffu;
-      if (lane == 0) masks[warp][s] = m;
+      const Tile tl = src.tile(i);
+      load_codes<D, KB, ALIGNED>(dst, kc, tl);
+      load_codes<D, VB, ALIGNED>(dst + RB::K + RB::S, vc, tl);
+      load_scales<D, ALIGNED>(dst + sc_dst, sc_pool, tl, lane & 15);
+      if (lane == 0) masks[warp][s] = tl.mask;
     }
     cp_async_commit();
   };

@@ -33,7 +33,8 @@ using namespace qt;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 4;
-constexpr int kChunk = 512;          // tokens a CTA
+constexpr int kChunk = 512;          // tokens a CTA, two a thread
+constexpr int kMaxRecv = 16;         // receivers a CTA
 constexpr int kPad = 4;              // floats between the receivers' weight rows
 
 struct MappedParams {
@@ -54,12 +55,6 @@ struct MappedParams {
   unsigned int* status;
 };
 
-// Two fp16 parts of w f: low half h, high half l.
-__device__ __forceinline__ float2 split_f16(float v) {
-  const float h = __half2float(__float2half_rn(v));
-  return make_float2(h, v - h);
-}
-
 // Exponent k that brings the largest |w| (bits of a non-negative float) into [2^14, 2^15).
 __device__ __forceinline__ int boost_exp(uint32_t wmax) {
   return wmax == 0 || wmax >= 0x7f800000u ? 0 : 14 - ((int)(wmax >> 23) - 127);
@@ -75,6 +70,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
   constexpr int NG = D / 32, R = D * BITS / 8, SB = NG * 2, CT = GM == 2 ? 2 : 1;
   constexpr int kWarpBytes = kChunk * SB + kStages * kTok * R;
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int up_s[kMaxRecv];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tid = lane & 3;
 
   int u = blockIdx.x;
@@ -97,48 +93,80 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
   src.init(&p.v, b, hk, j0 + part * kTok, p.parts * kTok, live ? j0 + ntok : 0, p.status);
   srcs = src;
   // all scales of the unit's tokens first (a few KB): their largest sets the operand's scale
-  for (int i = 0; i < ntiles; ++i) {
-    const uint32_t row = srcs.rows(i);
-    if (lane < 16) load_scales<D>(scales + i * kTok * SB, p.v.scales, row);
-  }
+  for (int i = 0; i < ntiles; ++i)
+    load_scales<D, ALIGNED>(scales + i * kTok * SB, p.v.scales, srcs.tile(i), lane);
   cp_async_commit();
+  const uint8_t* vc = codes_base<D, BITS, ALIGNED>(p.v.codes);
   auto issue = [&](int i) {
     if (i < ntiles)
-      load_codes<D, BITS, ALIGNED>(ring + (i % kStages) * kTok * R, p.v.codes, src.rows(i));
+      load_codes<D, BITS, ALIGNED>(ring + (i % kStages) * kTok * R, vc, src.tile(i));
     cp_async_commit();
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue(i);
 
-  // the weights of the CTA's receivers: a token a thread, eight receivers at a time
+  // the weights of the CTA's receivers: two tokens a thread, eight receivers at a time
   const int recv = p.hs * p.rj;
-  for (int t = threadIdx.x; t < kChunk; t += kThreads) {
+  float* W_s = w_s + recv * (kChunk + kPad);               // [H_s][wcols], wcols a multiple of 8
+  const int wcols = (recv + 7) & ~7;
+  for (int e = threadIdx.x; e < p.H_s * wcols; e += kThreads) {
+    const int s = e / wcols, r = e - s * wcols, un = slice * p.hs + r / p.rj;
+    const int in = (un % p.rtiles) * p.rj + r % p.rj;        // receiver within its value head
+    const bool ok = r < recv && un < p.units && in < p.group;
+    W_s[e] = ok ? __ldg(p.W + ((int64_t)(un / p.rtiles) * p.group + in) * p.H_s + s) : 0.f;
+  }
+  __syncthreads();
+  {
+    const int t = threadIdx.x;
     const float* row = p.rows + (int64_t)b * p.H_s * p.stride + j0 + t;
+    const bool ok0 = t < ntok, ok1 = t + kThreads < ntok;
     for (int r0 = 0; r0 < recv; r0 += 8) {
-      const float* Wr[8];
-      float a[8];
+      float a[8], c[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int r = r0 + k, un = slice * p.hs + r / p.rj;
-        const int in = (un % p.rtiles) * p.rj + r % p.rj;      // receiver within its value head
-        const bool ok = r < recv && un < p.units && in < p.group;
-        Wr[k] = p.W + (ok ? (int64_t)(un / p.rtiles) * p.group + in : 0) * p.H_s;
-        a[k] = 0.f;
+      for (int k = 0; k < 8; ++k) a[k] = c[k] = 0.f;
+#pragma unroll 4
+      for (int s = 0; s < p.H_s; ++s) {
+        const float x = ok0 ? __ldg(row + (int64_t)s * p.stride) : 0.f;
+        const float y = ok1 ? __ldg(row + (int64_t)s * p.stride + kThreads) : 0.f;
+        const float4 u0 = *reinterpret_cast<const float4*>(W_s + s * wcols + r0);
+        const float4 u1 = *reinterpret_cast<const float4*>(W_s + s * wcols + r0 + 4);
+        const float wk[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[k] = fmaf(wk[k], x, a[k]), c[k] = fmaf(wk[k], y, c[k]);
       }
-      if (t < ntok)
-        for (int s = 0; s < p.H_s; ++s) {
-          const float x = __ldg(row + (int64_t)s * p.stride);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) a[k] = fmaf(__ldg(Wr[k] + s), x, a[k]);
-        }
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (r0 + k < recv) w_s[(r0 + k) * (kChunk + kPad) + t] = a[k];
+        if (r0 + k < recv) {
+          w_s[(r0 + k) * (kChunk + kPad) + t] = ok0 ? a[k] : 0.f;
+          w_s[(r0 + k) * (kChunk + kPad) + t + kThreads] = ok1 ? c[k] : 0.f;
+        }
     }
   }
   __syncthreads();
+  // each receiver's weights, times the power of two that brings the largest near 2^15, as two fp16 parts
+  // (high part in the low half) in place
+  for (int r = warp; r < recv; r += kWarps) {
+    float* w = w_s + r * (kChunk + kPad);
+    uint32_t m = 0;
+    float v[kChunk / 32];
+#pragma unroll
+    for (int k = 0; k < kChunk / 32; ++k) {
+      v[k] = w[lane + 32 * k];
+      m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    const int up = boost_exp(m);
+    const float up0 = pow2i(up / 2), up1 = pow2i(up - up / 2);
+#pragma unroll
+    for (int k = 0; k < kChunk / 32; ++k) {
+      const float x = v[k] * up0 * up1, h = __half2float(__float2half_rn(x));
+      reinterpret_cast<uint32_t*>(w)[lane + 32 * k] = pack_f16(h, x - h);
+    }
+    if (lane == 0) up_s[r] = up;
+  }
+  __syncthreads();
 
-  // largest scale of the unit's tokens, largest weight of each column's receiver
+  // largest scale of the unit's tokens
   cp_async_wait<kStages - 1>();
   __syncwarp();
   const int nrj = min(p.rj, p.group - rt * p.rj);            // receivers of this unit
@@ -164,30 +192,15 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
       __syncwarp();
     }
   }
-  const float* wr[CT];
-  float up0[CT], up1[CT];                                   // 2^k as a product of two floats
+  // this column's receiver (0 stands in for one that the unit lacks)
+  uint32_t wr[CT];
   int kexp[CT];
-  const int wbase = (warp % p.hs) * p.rj;
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
-    const int r = GM == 0 ? 0 : 4 * c + (gid >> 1);
-    const int rr = r < nrj ? r : 0;
-    wr[c] = w_s + (wbase + rr) * (kChunk + kPad);
-    uint32_t m = 0;
-    // the lanes of a receiver (two columns of four lanes; all 32 for GM 0) share its tokens
-    const int first = GM == 0 ? lane : lane & 7, step = GM == 0 ? 32 : 8;
-    for (int t = first; t < ntok; t += step) m = max(m, __float_as_uint(wr[c][t]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
-    if (GM == 0) {
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
-    }
-    kexp[c] = boost_exp(m);
-    up0[c] = pow2i(kexp[c] / 2);
-    up1[c] = pow2i(kexp[c] - kexp[c] / 2);
-    kexp[c] -= sdown;
+    int r = GM == 0 ? 0 : 4 * c + (gid >> 1);
+    r = (warp % p.hs) * p.rj + (r < nrj ? r : 0);
+    wr[c] = smem_u32(w_s + r * (kChunk + kPad) + part * kTok + tid);
+    kexp[c] = up_s[r] - sdown;
   }
 
   float o[CT][2 * NG][4];
@@ -204,20 +217,21 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
     __syncwarp();
     ValueTile<D, BITS> vt;
     vt.load(ring + (i % kStages) * kTok * R);
+    const uint32_t sp = scales + i * kTok * SB + tid * SB;   // tokens tid + 4 k
     uint2 sc[4];
+    if (GM != 0) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      sc[k] = lds_scales<NG>(scales + (i * kTok + tid + 4 * k) * SB);
-    const int t0 = (part + p.parts * i) * kTok + tid;
+      for (int k = 0; k < 4; ++k) sc[k] = lds_scales<NG>(sp + 4 * k * SB);
+    }
     uint32_t hp[CT][2], lp[CT][2];                          // weight pairs, high and low parts
 #pragma unroll
     for (int c = 0; c < CT; ++c)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float2 a = split_f16(wr[c][t0 + 8 * h] * up0[c] * up1[c]);
-        const float2 d = split_f16(wr[c][t0 + 8 * h + 4] * up0[c] * up1[c]);
-        hp[c][h] = pack_f16(a.x, d.x);
-        lp[c][h] = pack_f16(a.y, d.y);
+        const uint32_t at = wr[c] + i * p.parts * kTok * 4 + 32 * h;
+        const uint32_t a = lds32(at), d = lds32(at + 16);
+        hp[c][h] = __byte_perm(a, d, 0x5410);
+        lp[c][h] = __byte_perm(a, d, 0x7632);
       }
     auto weight = [&](int c, int h, uint32_t s) {
       const uint32_t p1 = hmul2(hp[c][h], s);
@@ -226,13 +240,10 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
     };
     uint32_t pb[CT][2];
     if (GM == 0) {
-      const int g = (gid >> 1) % NG;                        // this column's group
-      const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
-      const bool up = NG == 4 && g >= 2;
+      const uint32_t sg = sp + 2 * ((gid >> 1) % NG);       // this column's group
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        pb[0][h] = weight(0, h, __byte_perm(up ? sc[2 * h].y : sc[2 * h].x,
-                                            up ? sc[2 * h + 1].y : sc[2 * h + 1].x, sel));
+        pb[0][h] = weight(0, h, __byte_perm(lds16(sg + 8 * h * SB), lds16(sg + (8 * h + 4) * SB), 0x5410));
     }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -320,9 +331,9 @@ void mapped_shape(int H_kv, int group, int max_ctx, MappedParams* p) {
   p->rj = std::min(group, 8);
   p->rtiles = (group + p->rj - 1) / p->rj;
   p->units = H_kv * p->rtiles;
-  // at most 16 receivers a CTA keep their weights in 33 KB, so that two CTAs fit an SM
+  // at most kMaxRecv receivers a CTA keep their weights in 33 KB, so that two CTAs fit an SM
   p->hs = 1;
-  while (p->hs * 2 <= std::min(p->units, kWarps) && p->hs * 2 * p->rj <= 16) p->hs *= 2;
+  while (p->hs * 2 <= std::min(p->units, kWarps) && p->hs * 2 * p->rj <= kMaxRecv) p->hs *= 2;
   p->parts = kWarps / p->hs;
   p->slices = (p->units + p->hs - 1) / p->hs;
   p->chunks = std::max(1, (max_ctx + kChunk - 1) / kChunk);
@@ -331,7 +342,7 @@ void mapped_shape(int H_kv, int group, int max_ctx, MappedParams* p) {
 template <int D, int BITS, bool ALIGNED, int GM>
 int launch(const MappedParams& p, unsigned int blocks, cudaStream_t st) {
   const int bytes = kWarps * (kChunk * (D / 32) * 2 + kStages * kTok * D * BITS / 8) +
-                    p.hs * p.rj * (kChunk + kPad) * 4;
+                    p.hs * p.rj * (kChunk + kPad) * 4 + p.H_s * ((p.hs * p.rj + 7) & ~7) * 4;
   IAMAP_CUDA_CHECK(cudaFuncSetAttribute(quant_mapped_kernel<D, BITS, ALIGNED, GM>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
   quant_mapped_kernel<D, BITS, ALIGNED, GM><<<blocks, kThreads, bytes, st>>>(p);

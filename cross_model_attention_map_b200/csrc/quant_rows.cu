@@ -57,14 +57,14 @@ __global__ void __launch_bounds__(kThreads, 6) quant_rows_kernel(const RowsParam
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
   TileRows<ALIGNED> src;
   src.init(&p.k, b, hk, j0 + warp * kTok, kWarps * kTok, j1, p.status);
+  const uint8_t* kc = codes_base<D, BITS, ALIGNED>(p.k.codes);
   auto issue = [&](int i) {
     if (i < ntiles) {
       const int s = i % kStages;
-      const uint32_t row = src.rows(i);
-      load_codes<D, BITS, ALIGNED>(ring + s * kStage, p.k.codes, row);
-      if (lane < 16) load_scales<D>(ring + s * kStage + K, p.k.scales, row);
-      const uint32_t m = __ballot_sync(0xffffffffu, row != kNoRow) & 0xffffu;
-      if (lane == 0) masks[warp][s] = m;
+      const Tile tl = src.tile(i);
+      load_codes<D, BITS, ALIGNED>(ring + s * kStage, kc, tl);
+      load_scales<D, ALIGNED>(ring + s * kStage + K, p.k.scales, tl, lane);
+      if (lane == 0) masks[warp][s] = tl.mask;
     }
     cp_async_commit();
   };

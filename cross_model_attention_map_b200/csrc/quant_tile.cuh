@@ -45,6 +45,11 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
@@ -288,19 +293,24 @@ __device__ __forceinline__ uint32_t scale_pair(const uint2* sc, int g) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Where a tile's rows lie
+// Where a tile's rows lie, and their copies
 // ------------------------------------------------------------------------------------------------
 
-// Rows of the 16-token tiles of one (sequence, head), tile by tile: rows(i) gives the pool row of token
-// lane % 16 of the warp's i-th tile, kNoRow where the page is bad or the token at or past `end`.
-// ALIGNED: page_size is a multiple of 16, so a tile is 16 consecutive rows; lane l then looks up the
-// page of the warp's tile (base + l), 32 tiles at a time. Otherwise every token is looked up, one tile
-// ahead of its use.
+// A 16-token tile's rows in the pools: ALIGNED (page_size a multiple of 16), the first of 16
+// consecutive rows, the same in every lane; otherwise the row of token lane % 16. Bit t of mask says
+// that token t exists: below the end of the range, on a good page.
+struct Tile {
+  uint32_t row, mask;
+};
+
+// The tiles of one (sequence, head), tokens first + i * step .. of the warp's i-th tile. ALIGNED: lane l
+// looks up the page of tile (base + l), 32 tiles at a time; otherwise every token is looked up, one
+// tile ahead of its use.
 template <bool ALIGNED>
 struct TileRows {
   const QuantPages* p;
   const int32_t* table;
-  int head, first, step, end;     // tile i covers tokens first + i * step ..
+  int head, first, step, end;
   uint32_t held;
   int held_at;
   unsigned int* status;
@@ -325,42 +335,81 @@ struct TileRows {
     held = ALIGNED ? look(first + lane * step) : look(first + (lane & 15));
   }
   // Must be called with i = 0, 1, 2, ... by the whole warp.
-  __device__ __forceinline__ uint32_t rows(int i) {
-    const int lane = threadIdx.x & 31, t = lane & 15;
+  __device__ __forceinline__ Tile tile(int i) {
+    const int lane = threadIdx.x & 31;
+    Tile t;
     if (ALIGNED) {
       if (i - held_at == 32) {
         held_at = i;
         held = look(first + (i + lane) * step);
       }
-      const uint32_t r0 = __shfl_sync(0xffffffffu, held, i - held_at);
-      return r0 == kNoRow || first + i * step + t >= end ? kNoRow : r0 + t;
+      t.row = __shfl_sync(0xffffffffu, held, i - held_at);
+      const int left = end - (first + i * step);
+      t.mask = t.row == kNoRow ? 0u : left >= kTok ? 0xffffu : (1u << left) - 1u;
+    } else {
+      t.row = held;
+      t.mask = __ballot_sync(0xffffffffu, held != kNoRow) & 0xffffu;
+      held = look(first + (i + 1) * step + (lane & 15));
     }
-    const uint32_t r = held;
-    held = look(first + (i + 1) * step + t);
-    return r;
+    return t;
   }
 };
 
-// Starts the copy of one tile's codes and scales; `row` as TileRows::rows gives it.
+// Starts the copy of a tile's codes. `base` is the pool's codes plus 16 * lane where ALIGNED: a tile is
+// then one contiguous run, and 16-byte pieces lane, lane + 32, .. of it go to their places.
 template <int D, int BITS, bool ALIGNED>
-__device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* codes, uint32_t row) {
-  constexpr int R = D * BITS / 8, PER = R / 16;     // pieces a row
+__device__ __forceinline__ const uint8_t* codes_base(const uint8_t* codes) {
+  return ALIGNED ? codes + 16 * (threadIdx.x & 31) : codes;
+}
+template <int D, int BITS, bool ALIGNED>
+__device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* base, Tile tl) {
+  constexpr int R = D * BITS / 8, PER = R / 16, N = PER * kTok / 32;     // pieces a row, a lane
   const int lane = threadIdx.x & 31;
+  if constexpr (ALIGNED) {
+    const uint8_t* src = base + (uint64_t)tl.row * R;
+    if (tl.mask == 0xffffu) {
 #pragma unroll
-  for (int i = 0; i < PER * kTok / 32; ++i) {
-    const int id = i * 32 + lane, t = id / PER, c = id % PER;
-    const uint32_t r = __shfl_sync(0xffffffffu, row, t);
-    cp_async<16>(dst + tile_off<R>(t, c), codes + (r == kNoRow ? 0 : (uint64_t)r * R + c * 16),
-                 r != kNoRow);
+      for (int i = 0; i < N; ++i) {
+        const int id = i * 32 + lane;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(
+                         dst + tile_off<R>(id / PER, id % PER)),
+                     "l"(src + 512 * i));
+      }
+      return;
+    }
+    if (tl.mask == 0) src = base;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int id = i * 32 + lane;
+      cp_async<16>(dst + tile_off<R>(id / PER, id % PER), src + 512 * i, (tl.mask >> (id / PER)) & 1);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int id = i * 32 + lane, t = id / PER, c = id % PER;
+      const uint32_t r = __shfl_sync(0xffffffffu, tl.row, t);
+      cp_async<16>(dst + tile_off<R>(t, c), base + (r == kNoRow ? 0 : (uint64_t)r * R + c * 16),
+                   r != kNoRow);
+    }
   }
 }
-template <int D>
-__device__ __forceinline__ void load_scales(uint32_t dst, const __half* scales, uint32_t row) {
+
+// Starts the copy of a tile's scales by lanes first .. first + 15 (`lane16` is the lane's place among
+// them; the other lanes pass a place of 16 or more).
+template <int D, bool ALIGNED>
+__device__ __forceinline__ void load_scales(uint32_t dst, const __half* scales, Tile tl, int lane16) {
   constexpr int B = D / 32 * 2;
-  const int t = threadIdx.x & 15;
-  cp_async<B>(dst + t * B, reinterpret_cast<const uint8_t*>(scales) +
-                               (row == kNoRow ? 0 : (uint64_t)row * B),
-              row != kNoRow);
+  const uint8_t* src = reinterpret_cast<const uint8_t*>(scales);
+  if (ALIGNED && tl.mask == 0xffffu) {
+    if (lane16 < B)                            // 16 rows of B bytes are B pieces of 16
+      cp_async<16>(dst + lane16 * 16, src + (uint64_t)tl.row * B + lane16 * 16, true);
+    return;
+  }
+  if (lane16 < kTok) {
+    const bool ok = (tl.mask >> lane16) & 1;
+    const uint32_t row = ALIGNED ? tl.row + lane16 : tl.row;
+    cp_async<B>(dst + lane16 * B, src + (ok ? (uint64_t)row * B : 0), ok);
+  }
 }
 
 }  // namespace qt
