@@ -4,17 +4,18 @@
 //
 // Bound by the cache bytes (72 + 72 a token and head of 128 in 4 bits). One CTA takes a range of tokens
 // of one (sequence, key head) and up to eight of the query heads that share it; each of its four warps
-// streams every fourth 16-token tile through a ring of asynchronous copies of its own, so no barrier
-// stands in the loop, and keeps scores, softmax and output in registers:
+// streams every fourth step of 64 (or 32) tokens through a ring of copies of its own and keeps scores, softmax
+// and output in registers:
 //
 //   S^T = K^ q^T (codes; group scales in fp32), x = S / sqrt(d) in base 2, p = 2^(x - ref),
 //   O^T += V^T (p s) with s the token's scale of the group.
 //
 // ref is a reference near the running maximum, not the maximum itself: it moves only when a score
-// exceeds it by more than 15 (then to 8 below the new maximum), which is rare after the first tiles,
-// so most tiles need no reduction across lanes and no rescaling. p and p s are fp16 (11 bits; the
+// exceeds it by more than 14 (then to 8 below the new maximum), which is rare after the first steps,
+// so most steps need no reduction across lanes and no rescaling. p and p s are fp16 (11 bits; the
 // output has 8): between 2^-24 and 2^15, with at least one p of the warp's tokens near 2^8 or above.
-// A product p s beyond 2^15 (scales above 2^7 or so) raises ref by 16. l = sum p is fp32.
+// Scales of 2 and more could take p s beyond that: a step that holds one checks its products, and raises
+// the ref of a head whose products do. l = sum p is fp32.
 //
 // Ranges of one sequence are joined by a second kernel; a sequence that fits in one range is written by
 // the first.
@@ -30,7 +31,6 @@ using namespace qt;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 4;
 constexpr int kHeads = 8;            // query heads a CTA
 constexpr float kNoRef = -3e38f;
 
@@ -54,58 +54,43 @@ struct AttnParams {
 
 template <int D, int KB, int VB>
 struct Ring {
-  static constexpr int K = kTok * D * KB / 8, V = kTok * D * VB / 8, S = kTok * (D / 32) * 2;
-  static constexpr int kStage = K + V + 2 * S;
+  static constexpr int kRow = D * KB / 8 + D * VB / 8 + 2 * (D / 32) * 2;    // bytes a token
+  // Tiles a step: as many as leave three CTAs an SM two stages. Twelve warps an SM were as fast as
+  // sixteen with half the tiles, and need no spills.
+  static constexpr int kTiles = kRow <= 144 ? 4 : 2, kTokens = kTiles * kTok, kStages = 2;
+  static constexpr int K = kTokens * D * KB / 8, V = kTokens * D * VB / 8, S = kTokens * (D / 32) * 2;
+  static constexpr int kStage = K + S + V + S;           // keys' codes and scales, values'
   static constexpr int kWarp = kStages * kStage;
   static constexpr int kMerge = kWarps * kHeads * D * 4;
   static constexpr int kBytes = kWarps * kWarp > kMerge ? kWarps * kWarp : kMerge;
 };
 
 template <int D, int KB, int VB, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads, 4) quant_attention_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kThreads, 3) quant_attention_kernel(const AttnParams p) {
   using RB = Ring<D, KB, VB>;
-  constexpr int NG = D / 32;
+  constexpr int NG = D / 32, ST = RB::kStages, SB = NG * 2, TK = RB::kTokens;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint32_t masks[kWarps][kStages];
+  __shared__ StreamShared<RB::kTiles, ST> shared[kWarps];
   __shared__ float2 ml_s[kWarps][kHeads];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tid = lane & 3;
-  int u = blockIdx.x;
-  const int ht = u % p.htiles;
-  u /= p.htiles;
-  const int hk = u % p.k.H;
-  u /= p.k.H;
-  const int b = u % p.batch, split = u / p.batch;
+  const int hk = blockIdx.x / p.htiles, ht = blockIdx.x - hk * p.htiles, b = blockIdx.y, split = blockIdx.z;
   const int ctx = quant_ctx(p.ctx_lens, b, p.max_ctx, p.status);
-  const int nsplit = max(1, (ctx + p.chunk - 1) / p.chunk);
-  if (split >= nsplit) return;
   const int j0 = split * p.chunk, j1 = min(ctx, j0 + p.chunk);
+  if (j0 >= j1 && split > 0) return;
   const int h0 = hk * p.group + ht * kHeads;               // first query head of the CTA
   const int nh = min(kHeads, p.group - ht * kHeads);
+  const bool single = ctx <= p.chunk;                      // the only range of its sequence
 
-  // this warp's tiles: tokens j0 + 16 (warp + 4 i)
-  const int ntiles = max(0, (j1 - j0 + kTok - 1) / kTok - warp + kWarps - 1) / kWarps;
-  const uint32_t ring = smem_u32(smem) + warp * RB::kWarp;
-  TileRows<ALIGNED> src;
-  src.init(&p.k, b, hk, j0 + warp * kTok, kWarps * kTok, j1, p.status);
-  const uint8_t* kc = codes_base<D, KB, ALIGNED>(p.k.codes);
-  const uint8_t* vc = codes_base<D, VB, ALIGNED>(p.v_codes);
-  const __half* sc_pool = lane < 16 ? p.k.scales : p.v_scales;   // lanes 0..15 the keys' scales
-  const uint32_t sc_dst = lane < 16 ? RB::K : RB::K + RB::S + RB::V;
-  auto issue = [&](int i) {
-    if (i < ntiles) {
-      const int s = i % kStages;
-      const uint32_t dst = ring + s * RB::kStage;
-      const Tile tl = src.tile(i);
-      load_codes<D, KB, ALIGNED>(dst, kc, tl);
-      load_codes<D, VB, ALIGNED>(dst + RB::K + RB::S, vc, tl);
-      load_scales<D, ALIGNED>(dst + sc_dst, sc_pool, tl, lane & 15);
-      if (lane == 0) masks[warp][s] = tl.mask;
-    }
-    cp_async_commit();
-  };
+  Stream<ALIGNED, RB::kTiles, 4, ST> in;
+  in.init(&p.k, b, hk, j0 + warp * TK, kWarps * TK, j1, p.status,
+          smem_u32(smem) + warp * RB::kWarp, &shared[warp]);
+  in.template add<0>(p.k.codes, D * KB / 8);
+  in.template add<1>(p.k.scales, SB);
+  in.template add<2>(p.v_codes, D * VB / 8);
+  in.template add<3>(p.v_scales, SB);
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  for (int i = 0; i < ST - 1; ++i) in.fill(i);
 
   uint32_t qf[NG][4];
   float fq[2];
@@ -117,90 +102,143 @@ __global__ void __launch_bounds__(kThreads, 4) quant_attention_kernel(const Attn
 #pragma unroll
     for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
   float ref[2] = {kNoRef, kNoRef}, l[2] = {0.f, 0.f};
-  const int t0 = (gid >> 1) + 4 * (gid & 1);               // tokens of this lane's score rows: t0, t0 + 8
+  float most[2] = {kNoRef, kNoRef};                        // (ref + 14) / fq: the largest score that ref serves
+  const int t0 = (gid >> 1) + 4 * (gid & 1);               // tokens of a tile in this lane's score rows: t0, t0 + 8
 
-  for (int i = 0; i < ntiles; ++i) {
-    cp_async_wait<kStages - 2>();
-    __syncwarp();
-    const uint32_t st = ring + (i % kStages) * RB::kStage;
-    const uint32_t mask = masks[warp][i % kStages];
-    float x[4];
-    tile_scores<D, KB>(st, st + RB::K, qf, x);
+  for (int i = 0; i < in.nsteps; ++i) {
+    in.fill(i + ST - 1);
+    uint32_t st;
+    const uint32_t* masks;
+    if (!in.take(&st, &masks)) break;
+    const uint32_t vs = st + RB::K + RB::S;
+    // a scale of 2 or more, infinite or NaN among the step's values
+    const uint4 all = lds128(vs + RB::V + lane * 16 % RB::S);
+    const bool large = __any_sync(0xffffffffu, (all.x | all.y | all.z | all.w) & 0x40004000u);
+#pragma unroll 1
+    for (int h = 0; h < RB::kTiles / 2; ++h) {
+      const uint32_t mask = masks[h];
+      // scores of two tiles, to be multiplied by fq: x[t][c], c = 0, 1 row gid, 2, 3 row gid + 8
+      float x[2][4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] *= fq[c & 1];
-    if (mask != 0xffffu) {
-      if (!((mask >> t0) & 1)) x[0] = x[1] = -INFINITY;
-      if (!((mask >> (t0 + 8)) & 1)) x[2] = x[3] = -INFINITY;
-    }
-    if (__any_sync(0xffffffffu, fmaxf(x[0], x[2]) > ref[0] + 15.f || fmaxf(x[1], x[3]) > ref[1] + 15.f)) {
+      for (int t = 0; t < 2; ++t)
+        tile_scores<D, KB>(st + (2 * h + t) * (kTok * D * KB / 8), st + RB::K + (2 * h + t) * (kTok * SB), qf,
+                           x[t]);
+      uint2 sc[2][4];                                      // the values' scales of tokens tid + 4 k
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float m = fmaxf(x[c], x[c + 2]);
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        if (m > ref[c] + 15.f) {
-          const float f = ex2(ref[c] - (m - 8.f));
-          ref[c] = m - 8.f;
-          l[c] *= f;
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int k = 0; k < 2 * NG; ++k) o[k][c] *= f, o[k][c + 2] *= f;
+        for (int k = 0; k < 4; ++k)
+          sc[t][k] = lds_scales<NG>(vs + RB::V + (32 * h + 16 * t + tid + 4 * k) * SB);
+      if (mask != 0xffffffffu) {
+        // tokens that do not exist: no probability, and no scale (memory behind them may hold anything)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!((mask >> (16 * t + t0)) & 1)) x[t][0] = x[t][1] = -INFINITY;
+          if (!((mask >> (16 * t + t0 + 8)) & 1)) x[t][2] = x[t][3] = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (!((mask >> (16 * t + tid + 4 * k)) & 1)) sc[t][k] = make_uint2(0, 0);
+        }
+      }
+      const float m0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+      const float m1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+      const bool slow = __any_sync(0xffffffffu, m0 > most[0] || m1 > most[1] || large);
+      if (slow) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float m = c ? m1 : m0;
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          if (m > most[c]) {
+            const float r = fmaf(m, fq[c], -8.f), f = ex2(ref[c] - r);
+            ref[c] = r;
+            most[c] = (r + 14.f) / fq[c];
+            l[c] *= f;
+#pragma unroll
+            for (int k = 0; k < 2 * NG; ++k) o[k][c] *= f, o[k][c + 2] *= f;
+          }
+        }
+      }
+      // probabilities as the operand of the second product: pb[t][0] tokens (tid, tid + 4), [1] + 8
+      uint32_t pb[2][2];
+      float e[2][4];
+      auto probabilities = [&]() {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          pb[t][0] = movmatrix_trans(pack_f16(e[t][0], e[t][1]));
+          pb[t][1] = movmatrix_trans(pack_f16(e[t][2], e[t][3]));
+        }
+      };
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) e[t][c] = ex2(fmaf(x[t][c], fq[c & 1], -ref[c & 1]));
+      probabilities();
+      if (large) {
+        __half2 top = __float2half2_rn(0.f);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t w = hmul2(pb[t][k], scale_pair(sc[t] + 2 * k, g));
+              top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&w)));
+            }
+        if (__any_sync(0xffffffffu,
+                       __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f)))) {
+          // column gid's largest product, and the power of two that brings it under 2^14
+          float big = 0.f;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float2 a = unpack_f16(pb[t][k]), s = unpack_f16(scale_pair(sc[t] + 2 * k, g));
+                const float u = fabsf(a.x * s.x), v = fabsf(a.y * s.y);
+                big = fmaxf(big, fmaxf(u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f));
+              }
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          const int down = big > 32768.f ? (int)(__float_as_uint(big) >> 23) - 127 - 13 : 0;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int n = __shfl_sync(0xffffffffu, down, 8 * tid + 4 * c);
+            if (n == 0) continue;
+            const float f = __uint_as_float((uint32_t)(127 - n) << 23);
+            ref[c] += (float)n;
+            most[c] = (ref[c] + 14.f) / fq[c];
+            l[c] *= f;
+#pragma unroll
+            for (int k = 0; k < 2 * NG; ++k) o[k][c] *= f, o[k][c + 2] *= f;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) e[t][c] *= f, e[t][c + 2] *= f;
+          }
+          probabilities();
+        }
+      }
+      l[0] += (e[0][0] + e[0][2]) + (e[1][0] + e[1][2]);
+      l[1] += (e[0][1] + e[0][3]) + (e[1][1] + e[1][3]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        ValueTile<D, VB> vt;
+        vt.load(vs + (2 * h + t) * (kTok * D * VB / 8));
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t w0 = hmul2(pb[t][0], scale_pair(sc[t], g));
+          const uint32_t w1 = hmul2(pb[t][1], scale_pair(sc[t] + 2, g));
+          uint32_t r[4], q[4];
+          vt.group(g, r, q);
+          mma_f16(o[2 * g], r[0], r[1], q[0], q[1], w0, w1);
+          mma_f16(o[2 * g + 1], r[2], r[3], q[2], q[3], w0, w1);
         }
       }
     }
-    float e[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) e[c] = ex2(x[c] - ref[c & 1]);
-
-    // value operands and the weights p s
-    const uint32_t vs = st + RB::K + RB::S;
-    ValueTile<D, VB> vt;
-    vt.load(vs);
-    uint2 sc[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) sc[k] = lds_scales<NG>(vs + RB::V + (tid + 4 * k) * (2 * NG));
-    uint32_t pb[NG][2];
-    auto weights = [&]() {
-      const uint32_t b0 = movmatrix_trans(pack_f16(e[0], e[1]));
-      const uint32_t b1 = movmatrix_trans(pack_f16(e[2], e[3]));
-      __half2 most = __float2half2_rn(0.f);
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        pb[g][0] = hmul2(b0, scale_pair(sc, g));
-        pb[g][1] = hmul2(b1, scale_pair(sc + 2, g));
-        most = __hmax2(most, __hmax2(*reinterpret_cast<__half2*>(&pb[g][0]),
-                                     *reinterpret_cast<__half2*>(&pb[g][1])));
-      }
-      return __hmax(__low2half(most), __high2half(most));
-    };
-    if (__any_sync(0xffffffffu, __hgt(weights(), __float2half(32768.f)))) {
-      constexpr float kDown = 1.f / 65536.f;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) e[c] *= kDown;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        ref[c] += ref[c] > kNoRef ? 16.f : 0.f;
-        l[c] *= kDown;
-      }
-#pragma unroll
-      for (int k = 0; k < 2 * NG; ++k)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[k][c] *= kDown;
-      weights();
-    }
-    l[0] += e[0] + e[2];
-    l[1] += e[1] + e[3];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      uint32_t r[4], t[4];
-      vt.group(g, r, t);
-      mma_f16(o[2 * g], r[0], r[1], t[0], t[1], pb[g][0], pb[g][1]);
-      mma_f16(o[2 * g + 1], r[2], r[3], t[2], t[3], pb[g][0], pb[g][1]);
-    }
     __syncwarp();
-    issue(i + kStages - 1);
   }
-  cp_async_wait<0>();
+  if (!ALIGNED) cp_async_wait<0>();
 
   // join the four warps
 #pragma unroll
@@ -240,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 4) quant_attention_kernel(const Attn
       const float4 t = *reinterpret_cast<const float4*>(o_s + w * kHeads * D + at);
       a.x += t.x, a.y += t.y, a.z += t.z, a.w += t.w;
     }
-    if (nsplit == 1) {
+    if (single) {
       const float inv = z == 0.f ? 0.f : 1.f / z;
       const int64_t row = (int64_t)b * p.Hq + h0 + h;
       *reinterpret_cast<uint2*>(p.out + row * D + (at - h * D)) =
@@ -287,13 +325,14 @@ __global__ void __launch_bounds__(D) quant_attention_join_kernel(const AttnParam
   if (p.lse && threadIdx.x == 0) p.lse[row] = z == 0.f ? -INFINITY : (m + log2f(z)) * kLn2;
 }
 
-// Ranges: enough CTAs to fill the device's 148 SMs four times over, at least 64 tokens (a tile a warp)
-// and at most 2048 each, so that one long sequence in a ragged batch is still spread.
+// Ranges: enough CTAs to fill the device's 148 SMs three times over, at least 256 tokens (a step a
+// warp) and at most 2048 each, so that one long sequence in a ragged batch is still spread.
 void attention_split(int batch, int units, int max_ctx, int* chunk, int* splits) {
   const int64_t total = (int64_t)units * max_ctx;
-  int64_t c = (total + 148 * 4 - 1) / (148 * 4);
-  c = (c + 63) / 64 * 64;
-  *chunk = (int)std::min<int64_t>(2048, std::max<int64_t>(64, c));
+  int64_t c = (total + 148 * 3 - 1) / (148 * 3);
+  c = (c + 255) / 256 * 256;
+  *chunk = (int)std::min<int64_t>(2048, std::max<int64_t>(256, c));
+  while ((max_ctx - 1) / *chunk >= 65535) *chunk *= 2;      // the grid's third dimension
   *splits = std::max(1, (max_ctx + *chunk - 1) / *chunk);
 }
 
@@ -304,12 +343,13 @@ size_t attention_bytes(int64_t units, int splits, int hpu, int D, size_t* ml_at)
 }
 
 template <int D, int KB, int VB, bool ALIGNED>
-int launch(const AttnParams& p, unsigned int blocks, cudaStream_t st) {
+int launch(const AttnParams& p, cudaStream_t st) {
   constexpr int bytes = Ring<D, KB, VB>::kBytes;
   if (bytes > 48 * 1024)
     IAMAP_CUDA_CHECK(cudaFuncSetAttribute(quant_attention_kernel<D, KB, VB, ALIGNED>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-  quant_attention_kernel<D, KB, VB, ALIGNED><<<blocks, kThreads, bytes, st>>>(p);
+  const dim3 grid(p.k.H * p.htiles, p.batch, p.splits);
+  quant_attention_kernel<D, KB, VB, ALIGNED><<<grid, kThreads, bytes, st>>>(p);
   IAMAP_LAUNCH_CHECK("quant_attention_kernel");
   if (p.splits > 1) {
     quant_attention_join_kernel<D><<<p.batch * p.Hq, D, 0, st>>>(p);
@@ -318,14 +358,14 @@ int launch(const AttnParams& p, unsigned int blocks, cudaStream_t st) {
   return IAMAP_OK;
 }
 template <int D, int KB, int VB>
-int launch_a(const AttnParams& p, unsigned int blocks, cudaStream_t st) {
-  return p.k.page_size % kTok == 0 ? launch<D, KB, VB, true>(p, blocks, st)
-                                   : launch<D, KB, VB, false>(p, blocks, st);
+int launch_a(const AttnParams& p, cudaStream_t st) {
+  return p.k.page_size % kTok == 0 ? launch<D, KB, VB, true>(p, st)
+                                   : launch<D, KB, VB, false>(p, st);
 }
 template <int D>
-int launch_d(const AttnParams& p, int kb, int vb, unsigned int blocks, cudaStream_t st) {
-  if (kb == 4) return vb == 4 ? launch_a<D, 4, 4>(p, blocks, st) : launch_a<D, 4, 8>(p, blocks, st);
-  return vb == 4 ? launch_a<D, 8, 4>(p, blocks, st) : launch_a<D, 8, 8>(p, blocks, st);
+int launch_d(const AttnParams& p, int kb, int vb, cudaStream_t st) {
+  if (kb == 4) return vb == 4 ? launch_a<D, 4, 4>(p, st) : launch_a<D, 4, 8>(p, st);
+  return vb == 4 ? launch_a<D, 8, 4>(p, st) : launch_a<D, 8, 8>(p, st);
 }
 
 }  // namespace
@@ -374,11 +414,9 @@ extern "C" int iamap_attention_paged_quant(const void* q, const void* k_codes, c
   p.htiles = (p.group + kHeads - 1) / kHeads;
   p.hpu = std::min(p.group, kHeads);
   const int64_t units = (int64_t)batch * H_kv * p.htiles;
-  if (units > 0x7fffff || (int64_t)batch * H_q > 0x7fffffff)
-    return set_error(IAMAP_ERR_UNSUPPORTED, "batch times heads is too large");
+  if (batch > 65535 || units > 0x7fffff || (int64_t)batch * H_q > 0x7fffffff)
+    return set_error(IAMAP_ERR_UNSUPPORTED, "batch above 65535, or batch times heads too large");
   attention_split(batch, (int)units, max_ctx, &p.chunk, &p.splits);
-  if (units * p.splits > 0x7fffffff)
-    return set_error(IAMAP_ERR_UNSUPPORTED, "batch times heads times max_ctx is too large");
   size_t ml_at = 0;
   const size_t need = p.splits > 1 ? attention_bytes(units, p.splits, p.hpu, d, &ml_at) : 1;
   if (!ws || ws_bytes < need)
@@ -402,8 +440,7 @@ extern "C" int iamap_attention_paged_quant(const void* q, const void* k_codes, c
   p.acc = static_cast<float*>(ws);
   p.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + ml_at);
   p.status = ctx->status;
-  const unsigned int blocks = (unsigned int)(units * p.splits);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 64 ? launch_d<64>(p, k_bits, v_bits, blocks, st)
-                 : launch_d<128>(p, k_bits, v_bits, blocks, st);
+  return d == 64 ? launch_d<64>(p, k_bits, v_bits, st)
+                 : launch_d<128>(p, k_bits, v_bits, st);
 }

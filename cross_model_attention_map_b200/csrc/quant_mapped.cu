@@ -5,7 +5,7 @@
 // Bound by the value bytes (72 a token and head of 128 in 4 bits). A CTA takes a range of tokens of one
 // sequence and up to eight units, a unit being a value head with up to eight of the receiver heads that
 // read it. First the CTA forms w of its receivers and tokens in shared memory (fp32); then each warp
-// streams the 16-token tiles of one unit through a ring of asynchronous copies.
+// streams the tokens of one unit through a ring of copies, 32 at a time.
 //
 // The product runs on matrix instructions with the codes as one operand (quant_tile.cuh). Its other
 // operand, the weight times the token's scale of the group, has to keep fp32's precision in fp16, so it
@@ -32,7 +32,6 @@ using namespace qt;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 4;
 constexpr int kChunk = 512;          // tokens a CTA, two a thread
 constexpr int kMaxRecv = 16;         // receivers a CTA
 constexpr int kPad = 4;              // floats between the receivers' weight rows
@@ -64,12 +63,21 @@ __device__ __forceinline__ float pow2i(int k) {
   return __uint_as_float((uint32_t)(min(max(k, -126), 127) + 127) << 23);
 }
 
+template <int D, int BITS>
+struct Ring {
+  static constexpr int kStage = kPair * D * BITS / 8;
+  static constexpr int kStages = kStage <= 2048 ? 3 : 2;
+  static constexpr int kWarp = kChunk * (D / 32) * 2 + kStages * kStage;   // scales and stages
+};
+
 // GM 0: group 1; GM 1, 2: up to four, eight receivers a unit.
 template <int D, int BITS, bool ALIGNED, int GM>
 __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedParams p) {
   constexpr int NG = D / 32, R = D * BITS / 8, SB = NG * 2, CT = GM == 2 ? 2 : 1;
-  constexpr int kWarpBytes = kChunk * SB + kStages * kTok * R;
+  using RB = Ring<D, BITS>;
+  constexpr int ST = RB::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ StreamShared<2, ST> shared[kWarps];
   __shared__ int up_s[kMaxRecv];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tid = lane & 3;
 
@@ -82,28 +90,26 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
   if (chunk >= nchunk) return;
   const int j0 = chunk * kChunk, ntok = min(ctx - j0, kChunk);
 
-  // this warp's unit and tiles: tokens j0 + 16 (part + parts i)
+  // this warp's unit and tokens: steps of 32 at j0 + 32 (part + parts i)
   const int unit = slice * p.hs + warp % p.hs, part = warp / p.hs;
   const bool live = unit < p.units;
   const int hk = live ? unit / p.rtiles : 0, rt = unit % p.rtiles;
-  const int ntiles = live ? max(0, (ntok + kTok - 1) / kTok - part + p.parts - 1) / p.parts : 0;
-  float* w_s = reinterpret_cast<float*>(smem + kWarps * kWarpBytes);
-  const uint32_t scales = smem_u32(smem) + warp * kWarpBytes, ring = scales + kChunk * SB;
-  TileRows<ALIGNED> src, srcs;
-  src.init(&p.v, b, hk, j0 + part * kTok, p.parts * kTok, live ? j0 + ntok : 0, p.status);
-  srcs = src;
+  float* w_s = reinterpret_cast<float*>(smem + kWarps * RB::kWarp);
+  const uint32_t scales = smem_u32(smem) + warp * RB::kWarp;   // the unit's scales, step after step
+  Stream<ALIGNED, 2, 1, ST> in;
+  in.init(&p.v, b, hk, j0 + part * kPair, p.parts * kPair, live ? j0 + ntok : 0, p.status,
+          scales + kChunk * SB, &shared[warp]);
+  in.template add<0>(p.v.codes, R);
   // all scales of the unit's tokens first (a few KB): their largest sets the operand's scale
-  for (int i = 0; i < ntiles; ++i)
-    load_scales<D, ALIGNED>(scales + i * kTok * SB, p.v.scales, srcs.tile(i), lane);
+  for (int i = 0; i < in.nsteps; ++i) {
+    const uint32_t row = in.rows.at(j0 + (part + p.parts * i) * kPair + lane, p.status);
+    cp_async<SB>(scales + (i * kPair + lane) * SB,
+                 reinterpret_cast<const uint8_t*>(p.v.scales) + (row == kNoRow ? 0 : (uint64_t)row * SB),
+                 row != kNoRow);
+  }
   cp_async_commit();
-  const uint8_t* vc = codes_base<D, BITS, ALIGNED>(p.v.codes);
-  auto issue = [&](int i) {
-    if (i < ntiles)
-      load_codes<D, BITS, ALIGNED>(ring + (i % kStages) * kTok * R, vc, src.tile(i));
-    cp_async_commit();
-  };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  for (int i = 0; i < ST - 1; ++i) in.fill(i);
 
   // the weights of the CTA's receivers: two tokens a thread, eight receivers at a time
   const int recv = p.hs * p.rj;
@@ -167,11 +173,11 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
   __syncthreads();
 
   // largest scale of the unit's tokens
-  cp_async_wait<kStages - 1>();
+  cp_async_wait<ALIGNED ? 0 : ST - 1>();                     // the scales, started before the ring's copies
   __syncwarp();
   const int nrj = min(p.rj, p.group - rt * p.rj);            // receivers of this unit
   uint32_t smax = 0;
-  for (int e = lane * 4; e < ntiles * kTok * SB; e += 128) {
+  for (int e = lane * 4; e < in.nsteps * kPair * SB; e += 128) {
     const uint32_t v = lds32(scales + e) & 0x7fff7fffu;
     smax = __vmaxu2(smax, v & ~__vcmpgtu2(v, 0x7bff7bffu));   // infinities and NaN set no scale
   }
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
       // 2^-sdown in two factors that fp16 has (sdown is in [-23, 16])
       const uint32_t f0 = pack_f16(pow2i(-(sdown / 2)), pow2i(-(sdown / 2)));
       const uint32_t f1 = pack_f16(pow2i(-(sdown - sdown / 2)), pow2i(-(sdown - sdown / 2)));
-      for (int e = lane * 4; e < ntiles * kTok * SB; e += 128)
+      for (int e = lane * 4; e < in.nsteps * kPair * SB; e += 128)
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(scales + e),
                      "r"(hmul2(hmul2(lds32(scales + e), f0), f1))
                      : "memory");
@@ -199,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
   for (int c = 0; c < CT; ++c) {
     int r = GM == 0 ? 0 : 4 * c + (gid >> 1);
     r = (warp % p.hs) * p.rj + (r < nrj ? r : 0);
-    wr[c] = smem_u32(w_s + r * (kChunk + kPad) + part * kTok + tid);
+    wr[c] = smem_u32(w_s + r * (kChunk + kPad) + part * kPair + tid);
     kexp[c] = up_s[r] - sdown;
   }
 
@@ -212,59 +218,74 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
       for (int e = 0; e < 4; ++e) o[c][i][e] = 0.f;
   const bool lo = gid & 1;
 
-  for (int i = 0; i < ntiles; ++i) {
-    cp_async_wait<kStages - 2>();
-    __syncwarp();
-    ValueTile<D, BITS> vt;
-    vt.load(ring + (i % kStages) * kTok * R);
-    const uint32_t sp = scales + i * kTok * SB + tid * SB;   // tokens tid + 4 k
-    uint2 sc[4];
-    if (GM != 0) {
+  for (int i = 0; i < in.nsteps; ++i) {
+    in.fill(i + ST - 1);
+    uint32_t st;
+    const uint32_t* masks;
+    if (!in.take(&st, &masks)) break;
+    const uint32_t mask = masks[0];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sc[k] = lds_scales<NG>(sp + 4 * k * SB);
-    }
-    uint32_t hp[CT][2], lp[CT][2];                          // weight pairs, high and low parts
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t at = wr[c] + i * p.parts * kTok * 4 + 32 * h;
-        const uint32_t a = lds32(at), d = lds32(at + 16);
-        hp[c][h] = __byte_perm(a, d, 0x5410);
-        lp[c][h] = __byte_perm(a, d, 0x7632);
-      }
-    auto weight = [&](int c, int h, uint32_t s) {
-      const uint32_t p1 = hmul2(hp[c][h], s);
-      const uint32_t p2 = hfma2(lp[c][h], s, hfma2(hp[c][h], s, p1 ^ 0x80008000u));
-      return lo ? p2 : p1;
-    };
-    uint32_t pb[CT][2];
-    if (GM == 0) {
-      const uint32_t sg = sp + 2 * ((gid >> 1) % NG);       // this column's group
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        pb[0][h] = weight(0, h, __byte_perm(lds16(sg + 8 * h * SB), lds16(sg + (8 * h + 4) * SB), 0x5410));
-    }
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
+    for (int q = 0; q < 2; ++q) {
+      ValueTile<D, BITS> vt;
+      vt.load(st + q * kTok * R);
+      const uint32_t sp = scales + (i * kPair + q * kTok + tid) * SB;   // tokens tid + 4 k
+      uint2 sc[4];
       if (GM != 0) {
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) pb[c][h] = weight(c, h, scale_pair(sc + 2 * h, g));
+        for (int k = 0; k < 4; ++k) sc[k] = lds_scales<NG>(sp + 4 * k * SB);
       }
-      uint32_t r[4], t[4];
-      vt.group(g, r, t);
+      uint32_t hp[CT][2], lp[CT][2];                          // weight pairs, high and low parts
 #pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        mma_f16(o[c][2 * g], r[0], r[1], t[0], t[1], pb[c][0], pb[c][1]);
-        mma_f16(o[c][2 * g + 1], r[2], r[3], t[2], t[3], pb[c][0], pb[c][1]);
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t at = wr[c] + (i * p.parts * kPair + q * kTok) * 4 + 32 * h;
+          const uint32_t a = lds32(at), d = lds32(at + 16);
+          hp[c][h] = __byte_perm(a, d, 0x5410);
+          lp[c][h] = __byte_perm(a, d, 0x7632);
+        }
+      if (mask != 0xffffffffu) {
+        // tokens that do not exist: no weight (their scales are 0, their codes may be anything)
+        const uint32_t m = mask >> (q * kTok + tid);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t keep = ((m >> (8 * h)) & 1 ? 0xffffu : 0u) | ((m >> (8 * h + 4)) & 1 ? 0xffff0000u : 0u);
+#pragma unroll
+          for (int c = 0; c < CT; ++c) hp[c][h] &= keep, lp[c][h] &= keep;
+        }
+      }
+      auto weight = [&](int c, int h, uint32_t s) {
+        const uint32_t p1 = hmul2(hp[c][h], s);
+        const uint32_t p2 = hfma2(lp[c][h], s, hfma2(hp[c][h], s, p1 ^ 0x80008000u));
+        return lo ? p2 : p1;
+      };
+      uint32_t pb[CT][2];
+      if (GM == 0) {
+        const uint32_t sg = sp + 2 * ((gid >> 1) % NG);       // this column's group
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          pb[0][h] = weight(0, h, __byte_perm(lds16(sg + 8 * h * SB), lds16(sg + (8 * h + 4) * SB), 0x5410));
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        if (GM != 0) {
+#pragma unroll
+          for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) pb[c][h] = weight(c, h, scale_pair(sc + 2 * h, g));
+        }
+        uint32_t r[4], t[4];
+        vt.group(g, r, t);
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          mma_f16(o[c][2 * g], r[0], r[1], t[0], t[1], pb[c][0], pb[c][1]);
+          mma_f16(o[c][2 * g + 1], r[2], r[3], t[2], t[3], pb[c][0], pb[c][1]);
+        }
       }
     }
     __syncwarp();
-    issue(i + kStages - 1);
   }
-  cp_async_wait<0>();
+  if (!ALIGNED) cp_async_wait<0>();
 
   // columns 2 tid, 2 tid + 1 are the two parts of receiver tid (GM 0: of group tid)
   const bool direct = nchunk == 1;
@@ -341,7 +362,7 @@ void mapped_shape(int H_kv, int group, int max_ctx, MappedParams* p) {
 
 template <int D, int BITS, bool ALIGNED, int GM>
 int launch(const MappedParams& p, unsigned int blocks, cudaStream_t st) {
-  const int bytes = kWarps * (kChunk * (D / 32) * 2 + kStages * kTok * D * BITS / 8) +
+  const int bytes = kWarps * Ring<D, BITS>::kWarp +
                     p.hs * p.rj * (kChunk + kPad) * 4 + p.H_s * ((p.hs * p.rj + 7) & ~7) * 4;
   IAMAP_CUDA_CHECK(cudaFuncSetAttribute(quant_mapped_kernel<D, BITS, ALIGNED, GM>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));

@@ -18,7 +18,6 @@ using namespace qt;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 4;
 constexpr int kHeads = 8;            // query heads a CTA
 constexpr float kNoRef = -3e38f;
 
@@ -36,65 +35,61 @@ struct RowsParams {
 };
 
 template <int D, int BITS, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads, 6) quant_rows_kernel(const RowsParams p) {
-  constexpr int NG = D / 32, K = kTok * D * BITS / 8, kStage = K + kTok * NG * 2;
-  __shared__ __align__(128) uint8_t smem[kWarps * kStages * kStage];
-  __shared__ uint32_t masks[kWarps][kStages];
+__global__ void __launch_bounds__(kThreads, 5) quant_rows_kernel(const RowsParams p) {
+  constexpr int NG = D / 32, SB = NG * 2, K = kPair * D * BITS / 8, kStage = K + kPair * SB;
+  constexpr int ST = kStage <= 2304 ? 4 : 2;
+  __shared__ __align__(128) uint8_t smem[kWarps * ST * kStage];
+  __shared__ StreamShared<2, ST> shared[kWarps];
   __shared__ float2 ml_s[kWarps][kHeads];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tid = lane & 3;
-  int u = blockIdx.x;
-  const int ht = u % p.htiles;
-  u /= p.htiles;
-  const int hk = u % p.k.H;
-  u /= p.k.H;
-  const int b = u % p.batch, split = u / p.batch;
+  const int hk = blockIdx.x / p.htiles, ht = blockIdx.x - hk * p.htiles, b = blockIdx.y, split = blockIdx.z;
   const int ctx = quant_ctx(p.ctx_lens, b, p.max_ctx, p.status);
   const int j0 = split * p.chunk, j1 = min(ctx, j0 + p.chunk);
   if (j0 >= j1) return;
   const int h0 = hk * p.group + ht * kHeads;
   const int nh = min(kHeads, p.group - ht * kHeads);
-  const int ntiles = max(0, (j1 - j0 + kTok - 1) / kTok - warp + kWarps - 1) / kWarps;
-  const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
-  TileRows<ALIGNED> src;
-  src.init(&p.k, b, hk, j0 + warp * kTok, kWarps * kTok, j1, p.status);
-  const uint8_t* kc = codes_base<D, BITS, ALIGNED>(p.k.codes);
-  auto issue = [&](int i) {
-    if (i < ntiles) {
-      const int s = i % kStages;
-      const Tile tl = src.tile(i);
-      load_codes<D, BITS, ALIGNED>(ring + s * kStage, kc, tl);
-      load_scales<D, ALIGNED>(ring + s * kStage + K, p.k.scales, tl, lane);
-      if (lane == 0) masks[warp][s] = tl.mask;
-    }
-    cp_async_commit();
-  };
+  Stream<ALIGNED, 2, 2, ST> in;
+  in.init(&p.k, b, hk, j0 + warp * kPair, kWarps * kPair, j1, p.status,
+          smem_u32(smem) + warp * ST * kStage, &shared[warp]);
+  in.template add<0>(p.k.codes, D * BITS / 8);
+  in.template add<1>(p.k.scales, SB);
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  for (int i = 0; i < ST - 1; ++i) in.fill(i);
   uint32_t qf[NG][4];
   float fq[2];
   load_query<D, BITS>(p.q + ((int64_t)b * p.Hq + h0) * D, nh, p.scale_log2, qf, fq);
   // a reference near the maximum, moved when a score exceeds it by more than 64 (sums stay in fp32)
   float ref[2] = {kNoRef, kNoRef}, l[2] = {0.f, 0.f};
   const int t0 = (gid >> 1) + 4 * (gid & 1);
-  float* row0 = p.rows + ((int64_t)b * p.Hq + h0 + 2 * tid) * p.stride + j0 + warp * kTok + t0;
+  const int jw = j0 + warp * kPair + t0;
+  float* row0 = p.rows + ((int64_t)b * p.Hq + h0 + 2 * tid) * p.stride + jw;
 
-  for (int i = 0; i < ntiles; ++i) {
-    cp_async_wait<kStages - 2>();
-    __syncwarp();
-    const uint32_t st = ring + (i % kStages) * kStage;
-    const uint32_t mask = masks[warp][i % kStages];
-    float x[4];
-    tile_scores<D, BITS>(st, st + K, qf, x);
+  for (int i = 0; i < in.nsteps; ++i) {
+    in.fill(i + ST - 1);
+    uint32_t st;
+    const uint32_t* masks;
+    if (!in.take(&st, &masks)) break;
+    const uint32_t mask = masks[0];
+    float x[2][4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] *= fq[c & 1];
-    if (mask != 0xffffu) {
-      if (!((mask >> t0) & 1)) x[0] = x[1] = -INFINITY;
-      if (!((mask >> (t0 + 8)) & 1)) x[2] = x[3] = -INFINITY;
+    for (int t = 0; t < 2; ++t) {
+      tile_scores<D, BITS>(st + t * (K / 2), st + K + t * (kTok * SB), qf, x[t]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[t][c] *= fq[c & 1];
     }
-    if (__any_sync(0xffffffffu, fmaxf(x[0], x[2]) > ref[0] + 64.f || fmaxf(x[1], x[3]) > ref[1] + 64.f)) {
+    if (mask != 0xffffffffu) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!((mask >> (16 * t + t0)) & 1)) x[t][0] = x[t][1] = -INFINITY;
+        if (!((mask >> (16 * t + t0 + 8)) & 1)) x[t][2] = x[t][3] = -INFINITY;
+      }
+    }
+    const float m0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+    const float m1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+    if (__any_sync(0xffffffffu, m0 > ref[0] + 64.f || m1 > ref[1] + 64.f)) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float m = fmaxf(x[c], x[c + 2]);
+        float m = c ? m1 : m0;
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -104,19 +99,21 @@ __global__ void __launch_bounds__(kThreads, 6) quant_rows_kernel(const RowsParam
         }
       }
     }
-    l[0] += ex2(x[0] - ref[0]) + ex2(x[2] - ref[0]);
-    l[1] += ex2(x[1] - ref[1]) + ex2(x[3] - ref[1]);
-    const int at = i * kWarps * kTok, j = j0 + warp * kTok + at + t0;
+    const int at = i * kWarps * kPair;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-      if (2 * tid + c < nh) {
-        if (j < j1) row0[(int64_t)c * p.stride + at] = x[c];
-        if (j + 8 < j1) row0[(int64_t)c * p.stride + at + 8] = x[c + 2];
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[c] += ex2(x[t][c] - ref[c]) + ex2(x[t][c + 2] - ref[c]);
+        if (2 * tid + c < nh) {
+          float* dst = row0 + (int64_t)c * p.stride + at + 16 * t;
+          if (jw + at + 16 * t < j1) dst[0] = x[t][c];
+          if (jw + at + 16 * t + 8 < j1) dst[8] = x[t][c + 2];
+        }
       }
     __syncwarp();
-    issue(i + kStages - 1);
   }
-  cp_async_wait<0>();
+  if (!ALIGNED) cp_async_wait<0>();
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     l[c] += __shfl_xor_sync(0xffffffffu, l[c], 4);
@@ -163,21 +160,23 @@ __global__ void __launch_bounds__(256) quant_rows_norm_kernel(const RowsParams p
 
 void rows_split(int units, int max_ctx, int* chunk, int* splits) {
   const int64_t total = (int64_t)units * max_ctx;
-  int64_t c = (total + 148 * 6 - 1) / (148 * 6);
-  c = (c + 63) / 64 * 64;
-  *chunk = (int)std::min<int64_t>(2048, std::max<int64_t>(64, c));
+  int64_t c = (total + 148 * 5 - 1) / (148 * 5);
+  c = (c + kWarps * kPair - 1) / (kWarps * kPair) * (kWarps * kPair);
+  *chunk = (int)std::min<int64_t>(2048, std::max<int64_t>(kWarps * kPair, c));
+  while ((max_ctx - 1) / *chunk >= 65535) *chunk *= 2;      // the grid's third dimension
   *splits = std::max(1, (max_ctx + *chunk - 1) / *chunk);
 }
 
 template <int D>
-int launch_d(const RowsParams& p, int bits, unsigned int blocks, cudaStream_t st) {
+int launch_d(const RowsParams& p, int bits, cudaStream_t st) {
   const bool al = p.k.page_size % kTok == 0;
+  const dim3 grid(p.k.H * p.htiles, p.batch, p.splits);
   if (bits == 4) {
-    if (al) quant_rows_kernel<D, 4, true><<<blocks, kThreads, 0, st>>>(p);
-    else quant_rows_kernel<D, 4, false><<<blocks, kThreads, 0, st>>>(p);
+    if (al) quant_rows_kernel<D, 4, true><<<grid, kThreads, 0, st>>>(p);
+    else quant_rows_kernel<D, 4, false><<<grid, kThreads, 0, st>>>(p);
   } else {
-    if (al) quant_rows_kernel<D, 8, true><<<blocks, kThreads, 0, st>>>(p);
-    else quant_rows_kernel<D, 8, false><<<blocks, kThreads, 0, st>>>(p);
+    if (al) quant_rows_kernel<D, 8, true><<<grid, kThreads, 0, st>>>(p);
+    else quant_rows_kernel<D, 8, false><<<grid, kThreads, 0, st>>>(p);
   }
   IAMAP_LAUNCH_CHECK("quant_rows_kernel");
   const int parts = (p.stride + kNormTokens - 1) / kNormTokens;
@@ -226,12 +225,10 @@ extern "C" int iamap_sender_rows_quant(const void* q, const void* k_codes, const
   p.group = H_s / H_k;
   p.htiles = (p.group + kHeads - 1) / kHeads;
   const int64_t units = (int64_t)batch * H_k * p.htiles;
-  if (units > 0x7fffff ||
+  if (batch > 65535 || units > 0x7fffff ||
       (int64_t)batch * H_s * ((ctx_stride + (int64_t)kNormTokens - 1) / kNormTokens) > 0x7fffffff)
-    return set_error(IAMAP_ERR_UNSUPPORTED, "batch times heads times ctx_stride is too large");
+    return set_error(IAMAP_ERR_UNSUPPORTED, "batch above 65535, or batch times heads times ctx_stride too large");
   rows_split((int)units, max_ctx, &p.chunk, &p.splits);
-  if (units * p.splits > 0x7fffffff)
-    return set_error(IAMAP_ERR_UNSUPPORTED, "batch times heads times max_ctx is too large");
   const size_t need = sizeof(float2) * (size_t)batch * H_s * p.splits;
   if (!ws || ws_bytes < need)
     return set_error(IAMAP_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws_bytes);
@@ -251,7 +248,6 @@ extern "C" int iamap_sender_rows_quant(const void* q, const void* k_codes, const
   p.stride = ctx_stride;
   p.ml = static_cast<float2*>(ws);
   p.status = ctx->status;
-  const unsigned int blocks = (unsigned int)(units * p.splits);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 64 ? launch_d<64>(p, bits, blocks, st) : launch_d<128>(p, bits, blocks, st);
+  return d == 64 ? launch_d<64>(p, bits, st) : launch_d<128>(p, bits, st);
 }

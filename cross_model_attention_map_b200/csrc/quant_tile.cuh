@@ -18,12 +18,15 @@
 // (for nibbles in the upper half of a byte 1024 + 16 u, one fused multiply-add).
 //
 // Row r of a 16-token tile is token (r & 8) + ((r & 7) >> 1) + 4 (r & 1): the two tokens of a pair of
-// columns 2 tid, 2 tid + 1 of P are then tokens tid and tid + 4 (+ 8), so that lanes of one load read
-// neighbouring rows. tile_off() places rows and 16-byte pieces so that both the keys' and the values'
-// loads are free of bank conflicts.
+// columns 2 tid, 2 tid + 1 of P are then tokens tid and tid + 4 (+ 8), so that the lanes of one load of
+// values read neighbouring rows. A tile lies in shared memory as in the pool, token after token, so one
+// bulk copy brings it where pages are multiples of 16 tokens; its loads have at worst two- (4 bits) or
+// four-way (values of 8 bits) bank conflicts, less than placing 16-byte pieces by address costs in
+// instructions.
 #pragma once
 
 #include "quant_cache.cuh"
+#include "tc_utils.cuh"
 
 namespace iamap {
 namespace qt {
@@ -31,39 +34,21 @@ namespace qt {
 constexpr uint32_t kNoRow = 0xffffffffu;
 constexpr int kTok = 16;                       // tokens a tile
 
-// Byte offset of 16-byte piece c of token t in a tile of R-byte rows.
-template <int R>
-__device__ __forceinline__ int tile_off(int t, int c) {
-  if (R == 128) return t * 128 + ((c ^ (((t & 3) << 1) | ((t >> 2) & 1))) << 4);
-  if (R == 64)
-    return (t >> 1) * 128 + (((t ^ (t >> 2)) & 1) << 6) + ((c ^ (((t >> 1) & 1) << 1)) << 4);
-  return (t ^ (((t >> 2) & 1) << 1)) * 32 + (c << 4);
-}
+constexpr int kPair = 2 * kTok;                // tokens of one mask
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
+// Loads from shared addresses. Plain loads, not asm: the compiler may move them among the matrix
+// instructions, but not across the waits (asm volatile would keep every one of them in place; the
+// attention kernel then took 165 us where it takes @@ now, 48 sequences of up to 16384 tokens).
+template <typename T>
+__device__ __forceinline__ T lds(uint32_t a) {
+  return *static_cast<const T*>(__cvta_shared_to_generic(a));
 }
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) { return lds<uint16_t>(a); }
+__device__ __forceinline__ uint32_t lds32(uint32_t a) { return lds<uint32_t>(a); }
+__device__ __forceinline__ uint2 lds64(uint32_t a) { return lds<uint2>(a); }
+__device__ __forceinline__ uint4 lds128(uint32_t a) { return lds<uint4>(a); }
 
-// Asynchronous copy of N (4, 8 or 16) bytes; zeros where !valid.
+// cp.async of N (4, 8 or 16) bytes; zeros where !valid.
 template <int N>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
   const int n = valid ? N : 0;
@@ -114,11 +99,18 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
 // D = A (16 x 16 fp16, row) . B (16 x 8 fp16, col) + D in fp32.
 __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// D = A . B
+__device__ __forceinline__ void mma_f16_first(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // The eight codes of a word of nibbles as fp16 pairs: r[i] = (nibble i, nibble 4 + i) - 8.
@@ -200,17 +192,17 @@ __device__ __forceinline__ void tile_scores(uint32_t codes, uint32_t scales, con
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int t = t0 + 8 * h;
+    const uint32_t at = codes + t * R + tid * (R / 4);
     if (R == 128) {
-      const uint4 a = lds128(codes + tile_off<R>(t, 2 * tid));
-      const uint4 b = lds128(codes + tile_off<R>(t, 2 * tid + 1));
-      w[h][0] = a.x, w[h][1] = a.y, w[h][2] = a.z, w[h][3] = a.w;
+      const uint4 a = lds128(at), b = lds128(at + 16);
+      w[h][0] = a.x, w[h][1] = a.y, w[h][2 % (R / 16)] = a.z, w[h][3 % (R / 16)] = a.w;
       w[h][4 % (R / 16)] = b.x, w[h][5 % (R / 16)] = b.y, w[h][6 % (R / 16)] = b.z,
       w[h][7 % (R / 16)] = b.w;
     } else if (R == 64) {
-      const uint4 a = lds128(codes + tile_off<R>(t, tid));
+      const uint4 a = lds128(at);
       w[h][0] = a.x, w[h][1] = a.y, w[h][2 % (R / 16)] = a.z, w[h][3 % (R / 16)] = a.w;
     } else {
-      const uint2 a = lds64(codes + tile_off<R>(t, tid >> 1) + 8 * (tid & 1));
+      const uint2 a = lds64(at);
       w[h][0] = a.x, w[h][1] = a.y;
     }
   }
@@ -231,8 +223,8 @@ __device__ __forceinline__ void tile_scores(uint32_t codes, uint32_t scales, con
         a[h][3] = byte_pair<0x4342>(w[h][(NG + g) % (R / 16)]);
       }
     }
-    float c[4] = {0.f, 0.f, 0.f, 0.f};
-    mma_f16(c, a[0][0], a[1][0], a[0][1], a[1][1], qf[g][0], qf[g][1]);
+    float c[4];
+    mma_f16_first(c, a[0][0], a[1][0], a[0][1], a[1][1], qf[g][0], qf[g][1]);
     mma_f16(c, a[0][2], a[1][2], a[0][3], a[1][3], qf[g][2], qf[g][3]);
     const float2 f0 = unpack_f16(g < 2 ? sc0.x : sc0.y), f1 = unpack_f16(g < 2 ? sc1.x : sc1.y);
     const float s0 = g & 1 ? f0.y : f0.x, s1 = g & 1 ? f1.y : f1.x;
@@ -252,15 +244,15 @@ struct ValueTile {
     const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int t = tid + 4 * i;
+      const uint32_t at = codes + (tid + 4 * i) * R + gid * (R / 8);
       if (R == 128) {
-        const uint4 a = lds128(codes + tile_off<R>(t, gid));
+        const uint4 a = lds128(at);
         w[i][0] = a.x, w[i][1 % N] = a.y, w[i][2 % N] = a.z, w[i][3 % N] = a.w;
       } else if (R == 64) {
-        const uint2 a = lds64(codes + tile_off<R>(t, gid >> 1) + 8 * (gid & 1));
+        const uint2 a = lds64(at);
         w[i][0] = a.x, w[i][1 % N] = a.y;
       } else {
-        w[i][0] = lds32(codes + tile_off<R>(t, gid >> 2) + 4 * (gid & 3));
+        w[i][0] = lds32(at);
       }
     }
   }
@@ -293,29 +285,16 @@ __device__ __forceinline__ uint32_t scale_pair(const uint2* sc, int g) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Where a tile's rows lie, and their copies
+// A warp's stream of tokens
 // ------------------------------------------------------------------------------------------------
 
-// A 16-token tile's rows in the pools: ALIGNED (page_size a multiple of 16), the first of 16
-// consecutive rows, the same in every lane; otherwise the row of token lane % 16. Bit t of mask says
-// that token t exists: below the end of the range, on a good page.
-struct Tile {
-  uint32_t row, mask;
-};
-
-// The tiles of one (sequence, head), tokens first + i * step .. of the warp's i-th tile. ALIGNED: lane l
-// looks up the page of tile (base + l), 32 tiles at a time; otherwise every token is looked up, one
-// tile ahead of its use.
-template <bool ALIGNED>
-struct TileRows {
+// Row of the pools that holds a token of one (sequence, head), or kNoRow: past `end`, or on a bad page
+// (which is reported).
+struct QuantRow {
   const QuantPages* p;
-  const int32_t* table;
-  int head, first, step, end;
-  uint32_t held;
-  int held_at;
-  unsigned int* status;
-
-  __device__ __forceinline__ uint32_t look(int pos) const {
+  const int32_t* table;            // of the sequence
+  int head, end;
+  __device__ __forceinline__ uint32_t at(int pos, unsigned int* status) const {
     if (pos >= end) return kNoRow;
     const int pi = pos / p->page_size;
     const int page = __ldg(table + pi);
@@ -325,92 +304,181 @@ struct TileRows {
     }
     return (uint32_t)(((int64_t)page * p->H + head) * p->page_size + (pos - pi * p->page_size));
   }
-  __device__ __forceinline__ void init(const QuantPages* pages, int seq, int head_, int first_,
-                                       int step_, int end_, unsigned int* st) {
-    p = pages;
-    table = pages->table + (int64_t)seq * pages->max_pages;
-    head = head_, first = first_, step = step_, end = end_, status = st;
-    held_at = 0;
-    const int lane = threadIdx.x & 31;
-    held = ALIGNED ? look(first + lane * step) : look(first + (lane & 15));
-  }
-  // Must be called with i = 0, 1, 2, ... by the whole warp.
-  __device__ __forceinline__ Tile tile(int i) {
-    const int lane = threadIdx.x & 31;
-    Tile t;
-    if (ALIGNED) {
-      if (i - held_at == 32) {
-        held_at = i;
-        held = look(first + (i + lane) * step);
-      }
-      t.row = __shfl_sync(0xffffffffu, held, i - held_at);
-      const int left = end - (first + i * step);
-      t.mask = t.row == kNoRow ? 0u : left >= kTok ? 0xffffu : (1u << left) - 1u;
-    } else {
-      t.row = held;
-      t.mask = __ballot_sync(0xffffffffu, held != kNoRow) & 0xffffu;
-      held = look(first + (i + 1) * step + (lane & 15));
-    }
-    return t;
-  }
 };
 
-// Starts the copy of a tile's codes. `base` is the pool's codes plus 16 * lane where ALIGNED: a tile is
-// then one contiguous run, and 16-byte pieces lane, lane + 32, .. of it go to their places.
-template <int D, int BITS, bool ALIGNED>
-__device__ __forceinline__ const uint8_t* codes_base(const uint8_t* codes) {
-  return ALIGNED ? codes + 16 * (threadIdx.x & 31) : codes;
-}
-template <int D, int BITS, bool ALIGNED>
-__device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* base, Tile tl) {
-  constexpr int R = D * BITS / 8, PER = R / 16, N = PER * kTok / 32;     // pieces a row, a lane
-  const int lane = threadIdx.x & 31;
-  if constexpr (ALIGNED) {
-    const uint8_t* src = base + (uint64_t)tl.row * R;
-    if (tl.mask == 0xffffu) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int id = i * 32 + lane;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(
-                         dst + tile_off<R>(id / PER, id % PER)),
-                     "l"(src + 512 * i));
-      }
-      return;
-    }
-    if (tl.mask == 0) src = base;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int id = i * 32 + lane;
-      cp_async<16>(dst + tile_off<R>(id / PER, id % PER), src + 512 * i, (tl.mask >> (id / PER)) & 1);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int id = i * 32 + lane, t = id / PER, c = id % PER;
-      const uint32_t r = __shfl_sync(0xffffffffu, tl.row, t);
-      cp_async<16>(dst + tile_off<R>(t, c), base + (r == kNoRow ? 0 : (uint64_t)r * R + c * 16),
-                   r != kNoRow);
-    }
-  }
-}
+// The barriers and masks of one warp's ring, and its abort flag.
+template <int TILES, int STAGES>
+struct StreamShared {
+  uint64_t full[STAGES];
+  uint32_t mask[STAGES][TILES / 2];      // which of 32 tokens exist
+  int abort_flag;
+};
 
-// Starts the copy of a tile's scales by lanes first .. first + 15 (`lane16` is the lane's place among
-// them; the other lanes pass a place of 16 or more).
-template <int D, bool ALIGNED>
-__device__ __forceinline__ void load_scales(uint32_t dst, const __half* scales, Tile tl, int lane16) {
-  constexpr int B = D / 32 * 2;
-  const uint8_t* src = reinterpret_cast<const uint8_t*>(scales);
-  if (ALIGNED && tl.mask == 0xffffu) {
-    if (lane16 < B)                            // 16 rows of B bytes are B pieces of 16
-      cp_async<16>(dst + lane16 * 16, src + (uint64_t)tl.row * B + lane16 * 16, true);
-    return;
+// Brings the tokens of one (sequence, head), TILES tiles at a time, into a ring of stages in shared
+// memory that belongs to one warp, so that warps run apart (a ring shared by the CTA's warps, filled in
+// turns, was slower: 198 against 165 us in attention at 48 sequences of up to 16384). Up to ARRAYS pools
+// with the same rows are brought together (keys' codes, their scales, ...), one after the other in a
+// stage. More tiles a step spread its bookkeeping.
+//
+// ALIGNED (page_size a multiple of 16): a tile of 16 tokens is one run of memory in each pool, and lane
+// a + ARRAYS * tile starts one bulk copy; completion is counted on the stage's mbarrier. Tokens past the
+// end of the range come with their tile and hold anything: what uses them masks them. Otherwise every
+// row is copied by itself in pieces of 16 (codes) or 4 or 8 (scales) bytes, and tokens that do not exist
+// are zeros.
+//
+// Page indices: ALIGNED, lane l looks up tile l of the next 32; otherwise lane l looks up token l of
+// each 32 of a step.
+template <bool ALIGNED, int TILES, int ARRAYS, int STAGES>
+struct Stream {
+  static_assert(TILES * ARRAYS <= 32 && TILES % 2 == 0 && 32 % TILES == 0, "one bulk copy a lane");
+  static constexpr int kTokens = TILES * kTok;
+  QuantRow rows;
+  unsigned int* status;
+  StreamShared<TILES, STAGES>* sh;
+  int first, step, nsteps;
+  uint32_t held, good;             // row of a tile, and which of the 32 tiles have one
+  uint32_t ring, stage_bytes, tile_bytes;
+  int s_in, s_out;                 // next stage to fill and to use
+  uint32_t parity;
+  // this lane's copy (ALIGNED): lanes below TILES * ARRAYS
+  const uint8_t* src;
+  uint32_t mul, dst;
+  // all arrays (otherwise)
+  const uint8_t* pool[ARRAYS];
+  uint32_t row_bytes[ARRAYS];
+
+  // Step i is tokens first + i * step .. + kTokens of the sequence, below `end`.
+  __device__ __forceinline__ void init(const QuantPages* pages, int seq, int head, int first_,
+                                       int step_, int end, unsigned int* st, uint32_t ring_,
+                                       StreamShared<TILES, STAGES>* shared) {
+    rows = QuantRow{pages, pages->table + (int64_t)seq * pages->max_pages, head, end};
+    first = first_, step = step_, status = st, sh = shared, ring = ring_;
+    nsteps = end > first ? (end - first + step - 1) / step : 0;
+    s_in = s_out = 0, parity = 0, stage_bytes = tile_bytes = 0, good = held = 0;
+    src = nullptr, mul = dst = 0;
+    const int lane = threadIdx.x & 31;
+    if (ALIGNED) {
+      if (lane < STAGES) tc::mbar_init(smem_u32(&sh->full[lane]), 1);
+      if (lane == 0) sh->abort_flag = 0;
+      tc::fence_barrier_init();
+    }
+    __syncwarp();
   }
-  if (lane16 < kTok) {
-    const bool ok = (tl.mask >> lane16) & 1;
-    const uint32_t row = ALIGNED ? tl.row + lane16 : tl.row;
-    cp_async<B>(dst + lane16 * B, src + (ok ? (uint64_t)row * B : 0), ok);
+  // Array A: its pool and the bytes of one row. Arrays are added in order 0, 1, ...
+  template <int A>
+  __device__ __forceinline__ void add(const void* base, uint32_t bytes) {
+    const int lane = threadIdx.x & 31;
+    if (ALIGNED) {
+      if (lane % ARRAYS == A) {
+        src = static_cast<const uint8_t*>(base);
+        mul = bytes;
+        dst = stage_bytes + lane / ARRAYS * kTok * bytes;
+      }
+    } else {
+      pool[A] = static_cast<const uint8_t*>(base);
+      row_bytes[A] = bytes;
+    }
+    stage_bytes += kTokens * bytes;
+    tile_bytes += kTok * bytes;
   }
-}
+
+  // Starts step i (called for i = 0, 1, ... by the whole warp; nothing past the last step). Steps
+  // 0 .. STAGES - 2 are started first; then step i + STAGES - 1 is started before step i is taken, into
+  // the stage that step i - 1 left (the warp has met since its last read).
+  __device__ __forceinline__ void fill(int i) {
+    const int lane = threadIdx.x & 31;
+    if (i < nsteps) {
+      const uint32_t stage = ring + s_in * stage_bytes;
+      if constexpr (ALIGNED) {
+        constexpr int kHeld = 32 / TILES;          // steps a lookup serves
+        const int k = i % kHeld * TILES;
+        if (k == 0) {
+          held = rows.at(first + (i + lane / TILES) * step + lane % TILES * kTok, status);
+          good = __ballot_sync(0xffffffffu, held != kNoRow);
+        }
+        const uint32_t row = __shfl_sync(0xffffffffu, held, k + lane / ARRAYS % TILES);
+        const uint32_t bar = smem_u32(&sh->full[s_in]);
+        if (lane < TILES * ARRAYS && row != kNoRow)
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                  stage + dst),
+              "l"(src + (uint64_t)row * mul), "r"(mul * kTok), "r"(bar)
+              : "memory");
+        if (lane == 0) {
+          const uint32_t g = good >> k;
+          const int left = rows.end - (first + i * step);
+#pragma unroll
+          for (int h = 0; h < TILES / 2; ++h) {
+            uint32_t m = (g >> (2 * h) & 1 ? 0xffffu : 0u) | (g >> (2 * h) & 2 ? 0xffff0000u : 0u);
+            if (left < (h + 1) * kPair) m &= left <= h * kPair ? 0u : (1u << (left - h * kPair)) - 1u;
+            sh->mask[s_in][h] = m;
+          }
+          // the arrival completes the phase once these bytes have come, before or after it
+          tc::mbar_expect_tx(bar, tile_bytes * __popc(g & ((1u << TILES) - 1u)));
+        }
+        __syncwarp();
+      } else {
+#pragma unroll 1
+        for (int h = 0; h < TILES / 2; ++h) {
+          const uint32_t row = rows.at(first + i * step + h * kPair + lane, status);
+          uint32_t at = stage;
+#pragma unroll
+          for (int a = 0; a < ARRAYS; ++a) {
+            const uint32_t rb = row_bytes[a], to = at + h * kPair * rb;
+            if (rb >= 32) {
+              for (uint32_t id = lane; id < 2 * rb; id += 32) {       // kPair * rb / 16 pieces
+                const uint32_t t = id * 16 / rb, c = id * 16 - t * rb;
+                const uint32_t r = __shfl_sync(0xffffffffu, row, t);
+                cp_async<16>(to + id * 16, pool[a] + (r == kNoRow ? 0 : (uint64_t)r * rb + c),
+                             r != kNoRow);
+              }
+            } else if (rb == 8) {
+              cp_async<8>(to + lane * 8, pool[a] + (row == kNoRow ? 0 : (uint64_t)row * 8), row != kNoRow);
+            } else {
+              cp_async<4>(to + lane * 4, pool[a] + (row == kNoRow ? 0 : (uint64_t)row * 4), row != kNoRow);
+            }
+            at += kTokens * rb;
+          }
+          const uint32_t m = __ballot_sync(0xffffffffu, row != kNoRow);
+          if (lane == 0) sh->mask[s_in][h] = m;
+        }
+        __syncwarp();
+      }
+      s_in = s_in + 1 == STAGES ? 0 : s_in + 1;
+    }
+    if (!ALIGNED) cp_async_commit();
+  }
+
+  // Waits for the next step: its stage's address, and where its masks are. False if the wait gave up
+  // (IAMAP_DEV_TIMEOUT is set): the stream is over, and its copies in flight have landed or been waited
+  // for.
+  __device__ __forceinline__ bool take(uint32_t* stage, const uint32_t** mask) {
+    if constexpr (ALIGNED) {
+      const uint32_t bar = smem_u32(&sh->full[s_out]);
+      bool ok = tc::mbar_try_wait(bar, parity);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = ok || tc::wait_bar(bar, parity, &sh->abort_flag, status);
+        if (!__all_sync(0xffffffffu, ok)) {
+          for (int k = 0; k < STAGES; ++k) {
+            tc::drain_bar(smem_u32(&sh->full[s_out]), parity);
+            s_out = s_out + 1 == STAGES ? 0 : s_out + 1;
+            if (s_out == 0) parity ^= 1;
+            if (s_out == s_in) break;
+          }
+          return false;
+        }
+      }
+    } else {
+      cp_async_wait<STAGES - 1>();
+      __syncwarp();
+    }
+    *stage = ring + s_out * stage_bytes;
+    *mask = sh->mask[s_out];
+    s_out = s_out + 1 == STAGES ? 0 : s_out + 1;
+    if (s_out == 0) parity ^= 1;
+    return true;
+  }
+};
 
 }  // namespace qt
 }  // namespace iamap
