@@ -3,7 +3,14 @@
 //
 //   m = max |x| of a group of 32,  s = fp16(min(m / Q, 65504)),  c = clamp(rint(x / s), -Q, Q)
 //
-// Both are bound by HBM: 2 + bits / 8 + 1 / 16 bytes an element.
+// Both are bound by HBM: 2 + bits / 8 + 1 / 16 bytes an element. At that rate an SM has some 100
+// instructions for every 8 elements of 32 lanes, so: a lane holds half a group (the scale, its reciprocal
+// and the addresses serve 16 elements), a quotient is one fused multiply-add and one addition, and a CTA
+// looks its tokens' places up once, while its loads are in flight. 40960 tokens of 40 heads of 128 in 4
+// bits, written and read back: @@ us of 1.07 GB (8 elements a lane with IEEE divisions and a lookup a
+// lane: 693 us; without those 361 us).
+#include <algorithm>
+
 #include "internal.h"
 #include "quant_cache.cuh"
 
@@ -11,6 +18,12 @@ namespace iamap {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kUnroll = 2;         // half-groups in flight a thread
+constexpr int kMaxTokens = 128;    // tokens a CTA
+
+// A row's place: the pool row of its head 0 (head h: h * page_size rows further), or
+constexpr int64_t kNoToken = -1;   // the row belongs to no sequence (a padded batch)
+constexpr int64_t kBadPlace = -2;  // its position or page is out of range
 
 struct CacheIoParams {
   const __nv_bfloat16* x;   // write: rows to quantise, x_stride elements apart
@@ -20,17 +33,17 @@ struct CacheIoParams {
   const int32_t* cu;        // [num_seqs + 1] rows of each sequence
   const int32_t* starts;    // [num_seqs] position of each sequence's first row
   int num_seqs;
-  int d;
+  int tokens;               // rows a CTA
+  int per;                  // half-groups a row: H * d / 16
+  uint32_t per_inv;         // ceil(2^32 / per)
   QuantPages pages;
   uint8_t* codes;           // write: pages.codes, pages.scales
   __half* scales;
   unsigned int* status;
 };
 
-// Cache row of packed row i and head h: -1 if the row belongs to no sequence (a padded batch),
-// -2 if its position or page is out of range.
-__device__ __forceinline__ int64_t place_of(const CacheIoParams& p, int64_t i, int h) {
-  if (i < p.cu[0] || i >= p.cu[p.num_seqs]) return -1;
+__device__ __forceinline__ int64_t place_of(const CacheIoParams& p, int64_t i) {
+  if (i >= p.n || i < p.cu[0] || i >= p.cu[p.num_seqs]) return kNoToken;
   int lo = 0, hi = p.num_seqs;          // cu[lo] <= i < cu[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -38,94 +51,235 @@ __device__ __forceinline__ int64_t place_of(const CacheIoParams& p, int64_t i, i
   }
   const int64_t pos = (int64_t)p.starts[lo] + (i - p.cu[lo]);
   if (pos < 0 || pos >= (int64_t)p.pages.max_pages * p.pages.page_size || pos > 0x7fffffff)
-    return -2;
-  const int64_t row = quant_row(p.pages, lo, h, (int)pos);
-  return row < 0 ? -2 : row;
+    return kBadPlace;
+  const int64_t row = quant_row(p.pages, lo, 0, (int)pos);
+  return row < 0 ? kBadPlace : row;
 }
 
-// Four lanes a group: each holds eight elements (two runs of four).
+// The places of the CTA's tokens; bad ones are reported.
+__device__ __forceinline__ void find_places(const CacheIoParams& p, int64_t i0, int64_t* place) {
+  for (int t = threadIdx.x; t < p.tokens; t += kThreads) {
+    place[t] = place_of(p, i0 + t);
+    if (place[t] == kBadPlace) raise_status(p.status, IAMAP_DEV_BAD_INDEX);
+  }
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Levels of eight elements w (bf16 pairs) under the scale whose reciprocal is r (within 1 ulp): x / s
+// rounded to even, exactly, plus the offset, in the low byte of each u. x r + 1536 is rounded to
+// multiples of 2^-13 and |x / s| < 128, so it is within 2^-13 of x / s + 1536. x has 8 significant bits and s at
+// most 11: x / s is a tie k + 1/2, which is then met exactly (the error before that rounding is below
+// 2^-15), or at least 2^-12 away from one, and stays on its side. The addition of 2^23 + 2^22 + offset -
+// 1536 rounds to an integer, ties to even (the offset is even).
 template <int BITS>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheIoParams p) {
-  constexpr int Q = BITS == 4 ? 7 : 127;
-  const int lanes = p.d / 8;                               // lanes a row
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
-  const int l = threadIdx.x % lanes, g = l >> 2, t = l & 3;
-  const int64_t i = unit / p.pages.H;
-  const int h = (int)(unit - i * p.pages.H);
-  const int64_t row = i < p.n ? place_of(p, i, h) : -1;
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  if (row >= 0)
-    raw = __ldcs(reinterpret_cast<const uint4*>(p.x + i * p.x_stride + (int64_t)h * p.d + 8 * l));
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  // largest magnitude by the bits: infinities and NaN compare above every finite value
-  uint32_t m = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  if (row == -2) raise_status(p.status, IAMAP_DEV_BAD_INDEX);
-  if (row < 0) return;
-  __half s = __float2half_rn(fminf(__fdiv_rn(__uint_as_float(m << 16), (float)Q), 65504.f));
-  if (m >= 0x7f80u) s = __ushort_as_half(0x7e00);          // a group with an infinity or NaN
-  const float sf = __half2float(s);
-  uint32_t u[8];
+__device__ __forceinline__ void levels(const uint32_t* w, float r, uint32_t* u) {
+  constexpr float kOff = 12582912.f + (BITS == 4 ? 8.f : 128.f) - 1536.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float x = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
-    const float c = sf > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x, sf)), (float)-Q), (float)Q) : 0.f;
-    u[e] = (uint32_t)((int)c + (BITS == 4 ? 8 : 128));
+    const float x = e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+    u[e] = __float_as_uint(__fadd_rn(__fmaf_rn(x, r, 1536.f), kOff));
   }
-  const int ng = p.d / kQuantGroup;
-  if (t == 0) p.scales[row * ng + g] = s;
-  if (BITS == 4) {
-    uint16_t* dst = reinterpret_cast<uint16_t*>(p.codes + row * (p.d / 2));
-    dst[(2 * t) * ng + g] = (uint16_t)(u[0] | u[1] << 4 | u[2] << 8 | u[3] << 12);
-    dst[(2 * t + 1) * ng + g] = (uint16_t)(u[4] | u[5] << 4 | u[6] << 8 | u[7] << 12);
-  } else {
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.codes + row * p.d);
-    dst[(2 * t) * ng + g] = u[0] | u[1] << 8 | u[2] << 16 | u[3] << 24;
-    dst[(2 * t + 1) * ng + g] = u[4] | u[5] << 8 | u[6] << 16 | u[7] << 24;
+}
+// The same where x / s may exceed Q: s is subnormal, saturated or 0.
+template <int BITS>
+__device__ __forceinline__ void levels_clamped(const uint32_t* w, float s, uint32_t* u) {
+  constexpr float Q = BITS == 4 ? 7.f : 127.f;
+  const float r = s > 0.f ? rcp(s) : 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+    const float t = s > 0.f ? fminf(fmaxf(__fmul_rn(x, r), -Q), Q) : 0.f;
+    u[e] = __float_as_uint(__fadd_rn(__fadd_rn(t, 1536.f), 12582912.f + (BITS == 4 ? 8.f : 128.f) - 1536.f));
+  }
+}
+// Low bytes of four words.
+__device__ __forceinline__ uint32_t low_bytes(const uint32_t* u) {
+  return __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+}
+
+// Lane 2 g + h of a row holds elements 8 h .. 8 h + 7 and 16 + 8 h .. of group g (so that the two lanes of
+// a group load whole sectors): its runs 2 h, 2 h + 1, 4 + 2 h and 5 + 2 h.
+template <int D, int BITS>
+__global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const CacheIoParams p) {
+  constexpr int L = D / 16, NG = D / kQuantGroup;
+  constexpr float Q = BITS == 4 ? 7.f : 127.f;
+  constexpr int RW = D * BITS / 32;                          // words of a row's codes
+  __shared__ int64_t place[kMaxTokens];
+  __shared__ __align__(16) uint32_t stage[kThreads / 32][32 / L][RW + 4];   // a warp's rows, with their scales
+  const int64_t i0 = (int64_t)blockIdx.x * p.tokens;
+  const int units = p.tokens * p.per;
+  const int lane = threadIdx.x & 31, l = threadIdx.x % L, g = l >> 1, h = l & 1;
+  const __nv_bfloat16* x0 = p.x + i0 * p.x_stride;
+  for (int base = 0; base < units; base += kThreads * kUnroll) {
+    uint32_t w[kUnroll][8];
+    int tok[kUnroll], rest[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int c = base + threadIdx.x + k * kThreads;
+      tok[k] = p.tokens == 1 ? 0 : (int)__umulhi((uint32_t)c, p.per_inv);
+      rest[k] = c - tok[k] * p.per;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[k][e] = 0;
+      if (c < units && i0 + tok[k] < p.n) {
+        const uint4* src =
+            reinterpret_cast<const uint4*>(x0 + tok[k] * p.x_stride + 16 * rest[k] - 8 * h);
+        const uint4 a = __ldcs(src), b = __ldcs(src + 2);
+        w[k][0] = a.x, w[k][1] = a.y, w[k][2] = a.z, w[k][3] = a.w;
+        w[k][4] = b.x, w[k][5] = b.y, w[k][6] = b.z, w[k][7] = b.w;
+      }
+    }
+    if (base == 0) {
+      find_places(p, i0, place);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int c = base + threadIdx.x + k * kThreads;
+      if (c - lane >= units) break;                          // the whole warp
+      const int64_t at = c < units ? place[tok[k]] : kNoToken;
+      // largest magnitude by the bits: infinities and NaN compare above every finite value
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = __vmaxu2(m, w[k][e] & 0x7fff7fffu);
+      m = max(m & 0xffffu, m >> 16);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      // m / Q lies no nearer than 2^-15 of itself to a border of fp16's rounding unless it is a number of
+      // fp16, so the product with fl(1 / Q) rounds as the quotient does
+      const float top = __uint_as_float(m << 16) * (1.f / Q);
+      __half s = __float2half_rn(fminf(top, 65504.f));
+      const bool odd = m >= 0x7f80u;                         // a group with an infinity or NaN
+      if (odd) s = __ushort_as_half(0x7e00);
+      const float sf = odd ? 0.f : __half2float(s);
+      uint32_t u[16];
+      if (sf >= 6.103515625e-05f && top <= 65504.f) {
+        const float r = rcp(sf);
+        levels<BITS>(w[k], r, u);
+        levels<BITS>(w[k] + 4, r, u + 8);
+      } else {
+        levels_clamped<BITS>(w[k], sf, u);
+        levels_clamped<BITS>(w[k] + 4, sf, u + 8);
+      }
+      // the row's bytes meet in shared memory and leave in order, 8 or 16 a lane (stored from where they
+      // are made, in pieces of 4 and 2, they took 2.2 times as long)
+      uint32_t* mine = stage[threadIdx.x / 32][lane / L];
+      if (BITS == 8) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) mine[(2 * h + r + (r & 2)) * NG + g] = low_bytes(u + 4 * r);
+      } else {
+        // two runs a word: nibbles e of bytes [u0 u2 u4 u6] and [u1 u3 u5 u7]
+        uint32_t v[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t a = low_bytes(u + 8 * r), b = low_bytes(u + 8 * r + 4);
+          v[r] = __byte_perm(a, b, 0x6420) + (__byte_perm(a, b, 0x7531) << 4);
+        }
+        // a stored word holds one run of an even group and of the next: the lanes of the two (two
+        // apart) exchange two runs, and the even one has runs 2h, 2h + 1, the odd one 4 + 2h, 5 + 2h
+        const bool odd_g = g & 1;
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, odd_g ? v[0] : v[1], 2);
+        const uint32_t lo = odd_g ? other : v[0], hi = odd_g ? v[1] : other;
+        uint32_t* to = mine + (2 * h + (odd_g ? 4 : 0)) * (NG / 2) + g / 2;
+        to[0] = __byte_perm(lo, hi, 0x5410);
+        to[NG / 2] = __byte_perm(lo, hi, 0x7632);
+      }
+      if (h == 0) reinterpret_cast<__half*>(mine + RW)[g] = s;
+      __syncwarp();
+      if (at >= 0) {
+        // pool row: at + head * page_size
+        const int64_t row = at + (uint32_t)(rest[k] / L) * (uint64_t)p.pages.page_size;
+        uint8_t* to = p.codes + row * (RW * 4);
+        if (BITS == 4)
+          reinterpret_cast<uint2*>(to)[l] = reinterpret_cast<const uint2*>(mine)[l];
+        else
+          reinterpret_cast<uint4*>(to)[l] = reinterpret_cast<const uint4*>(mine)[l];
+        if (l < NG / 2) reinterpret_cast<uint32_t*>(p.scales + row * NG)[l] = mine[RW + l];
+      }
+      __syncwarp();
+    }
   }
 }
 
-template <int BITS>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheIoParams p) {
-  const int lanes = p.d / 8;
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
-  const int l = threadIdx.x % lanes, g = l >> 2, t = l & 3;
-  const int64_t i = unit / p.pages.H;
-  const int h = (int)(unit - i * p.pages.H);
-  if (i >= p.n) return;
-  const int64_t row = place_of(p, i, h);
-  if (row == -1) return;                                   // rows behind the last sequence
-  uint4 o = make_uint4(0, 0, 0, 0);
-  if (row >= 0) {
-    const int ng = p.d / kQuantGroup;
-    const float s = __half2float(p.pages.scales[row * ng + g]);
-    float v[8];
-    if (BITS == 4) {
-      const uint16_t* src = reinterpret_cast<const uint16_t*>(p.pages.codes + row * (p.d / 2));
+// Byte e of w as c s = (32768 + offset + c) s - (32768 + offset) s: the fp32 number 0x47000000 | u << 8 is
+// 32768 + u, the second product is exact (24 bits), so the sum is c s exactly.
+__device__ __forceinline__ float level_value(uint32_t w, int e, float s, float minus) {
+  return __fmaf_rn(__uint_as_float(__byte_perm(w, 0x47000000u, 0x7604 | e << 4)), s, minus);
+}
+
+template <int D, int BITS>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheIoParams p) {
+  constexpr int L = D / 16, NG = D / kQuantGroup, W = BITS / 2;      // words of codes a lane
+  __shared__ int64_t place[kMaxTokens];
+  const int64_t i0 = (int64_t)blockIdx.x * p.tokens;
+  const int units = p.tokens * p.per;
+  const int lane = threadIdx.x & 31, l = threadIdx.x % L, g = l >> 1, h = l & 1;
+  const bool odd_g = g & 1;
+  find_places(p, i0, place);
+  __syncthreads();
+  __nv_bfloat16* out0 = p.out + i0 * (int64_t)p.per * 16;
+  for (int base = 0; base < units; base += kThreads * kUnroll) {
+    uint32_t w[kUnroll][W];
+    uint16_t sb[kUnroll];
+    int64_t at[kUnroll];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t c = src[(2 * t + r) * ng + g];
+    for (int k = 0; k < kUnroll; ++k) {
+      const int c = base + threadIdx.x + k * kThreads;
+      const int tok = p.tokens == 1 ? 0 : (int)__umulhi((uint32_t)c, p.per_inv);
+      at[k] = c < units ? place[tok] : kNoToken;
+      const int64_t row = at[k] + (uint32_t)((c - tok * p.per) / L) * (uint64_t)p.pages.page_size;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * r + e] = (float)((int)((c >> (4 * e)) & 15u) - 8) * s;
-      }
-    } else {
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.pages.codes + row * p.d);
+      for (int r = 0; r < W; ++r) w[k][r] = 0;
+      sb[k] = 0;
+      if (at[k] >= 0) {
+        // 4 bits: the words of runs 2h, 2h + 1 (even group) or 4 + 2h, 5 + 2h; 8 bits: all four
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(p.pages.codes + row * (D * BITS / 8)) +
+                              (BITS == 4 ? (2 * h + (odd_g ? 4 : 0)) * (NG / 2) + g / 2 : 2 * h * NG + g);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t c = src[(2 * t + r) * ng + g];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * r + e] = (float)((int)((c >> (8 * e)) & 255u) - 128) * s;
+        for (int r = 0; r < W; ++r) w[k][r] = __ldg(src + (BITS == 4 ? r * (NG / 2) : (r + (r & 2)) * NG));
+        sb[k] = __ldg(reinterpret_cast<const uint16_t*>(p.pages.scales) + row * NG + g);
       }
     }
-    o = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                   pack_bf16(v[6], v[7]));
-  } else {
-    raise_status(p.status, IAMAP_DEV_BAD_INDEX);
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int c = base + threadIdx.x + k * kThreads;
+      if (c - lane >= units) break;                          // the whole warp
+      const float s = __half2float(__ushort_as_half(sb[k]));
+      const float minus = -(BITS == 4 ? 32776.f : 32896.f) * s;
+      uint32_t o[8];
+      if (BITS == 4) {
+        const uint32_t mine = __byte_perm(w[k][0], w[k][1], odd_g ? 0x7632 : 0x5410);
+        const uint32_t give = __byte_perm(w[k][0], w[k][1], odd_g ? 0x5410 : 0x7632);
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 2);
+        const uint32_t runs[2] = {odd_g ? got : mine, odd_g ? mine : got};
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t a = runs[r] & 0x0f0f0f0fu, b = (runs[r] >> 4) & 0x0f0f0f0fu;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o[4 * r + e] = pack_bf16(level_value(a, e, s, minus), level_value(b, e, s, minus));
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            o[2 * r + e] = pack_bf16(level_value(w[k][r % W], 2 * e, s, minus),
+                                     level_value(w[k][r % W], 2 * e + 1, s, minus));
+      }
+      if (at[k] != kNoToken) {                               // rows behind the last sequence stay
+        uint4* dst = reinterpret_cast<uint4*>(out0 + 16 * (int64_t)c - 8 * h);
+        const bool ok = at[k] >= 0;
+        __stcs(dst, ok ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(0, 0, 0, 0));
+        __stcs(dst + 2, ok ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(0, 0, 0, 0));
+      }
+    }
   }
-  *reinterpret_cast<uint4*>(p.out + (i * p.pages.H + h) * p.d + 8 * l) = o;
 }
 
 int cache_io_check(const void* rows, const int32_t* cu, const int32_t* starts, int num_seqs,
@@ -138,11 +292,16 @@ int cache_io_check(const void* rows, const int32_t* cu, const int32_t* starts, i
   return IAMAP_OK;
 }
 
-int cache_io_grid(int64_t n, int H, int d, unsigned int* blocks) {
-  const int64_t per = kThreads / (d / 8);
-  const int64_t b = (n * H + per - 1) / per;
-  if (b > 0x7fffffff) return set_error(IAMAP_ERR_UNSUPPORTED, "too many rows for one call");
-  *blocks = (unsigned int)b;
+// Rows a CTA: up to eight rounds of its threads, so that the places' latency is met once for many rows,
+// but no more than leave six CTAs an SM.
+int cache_io_shape(int64_t n, int H, int d, CacheIoParams* p, unsigned int* blocks) {
+  const int64_t per = (int64_t)H * (d / 16);
+  if (per > 0x7fffffff / 2) return set_error(IAMAP_ERR_UNSUPPORTED, "too many heads");
+  p->per = (int)per;
+  const int64_t most = std::min<int64_t>(kMaxTokens, 4096 / per), spread = (n + 148 * 6 - 1) / (148 * 6);
+  p->tokens = (int)std::max<int64_t>(1, std::min(most, spread));
+  p->per_inv = (uint32_t)(((1ull << 32) + per - 1) / per);   // exact: used for numbers below 2^13 only
+  *blocks = (unsigned int)((n + p->tokens - 1) / p->tokens);
   return IAMAP_OK;
 }
 
@@ -190,29 +349,31 @@ extern "C" int iamap_cache_write(const void* x, int64_t x_stride, int64_t n, con
   if (rc) return rc;
   if (x_stride < (int64_t)H * d || x_stride % 8 != 0)
     return set_error(IAMAP_ERR_INVALID_ARG, "x_stride must be a multiple of 8, at least H * d");
+  CacheIoParams p{};
   unsigned int blocks = 0;
-  rc = cache_io_grid(n, H, d, &blocks);
+  rc = cache_io_shape(n, H, d, &p, &blocks);
   if (rc) return rc;
   if (blocks == 0) return IAMAP_OK;
   DeviceContext* ctx = device_context();
   if (!ctx) return IAMAP_ERR_CUDA;
-  CacheIoParams p{};
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.x_stride = x_stride;
   p.n = n;
   p.cu = cu;
   p.starts = starts;
   p.num_seqs = num_seqs;
-  p.d = d;
   p.codes = static_cast<uint8_t*>(codes);
   p.scales = static_cast<__half*>(scales);
   p.pages = QuantPages{p.codes, p.scales, num_pages, page_table, max_pages, page_size, H};
   p.status = ctx->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (bits == 4)
-    cache_write_kernel<4><<<blocks, kThreads, 0, st>>>(p);
-  else
-    cache_write_kernel<8><<<blocks, kThreads, 0, st>>>(p);
+  if (d == 64) {
+    if (bits == 4) cache_write_kernel<64, 4><<<blocks, kThreads, 0, st>>>(p);
+    else cache_write_kernel<64, 8><<<blocks, kThreads, 0, st>>>(p);
+  } else {
+    if (bits == 4) cache_write_kernel<128, 4><<<blocks, kThreads, 0, st>>>(p);
+    else cache_write_kernel<128, 8><<<blocks, kThreads, 0, st>>>(p);
+  }
   IAMAP_LAUNCH_CHECK("cache_write_kernel");
   return IAMAP_OK;
 }
@@ -226,27 +387,29 @@ extern "C" int iamap_cache_read(const void* codes, const void* scales, int64_t n
   if (rc) return rc;
   rc = cache_io_check(out, cu, starts, num_seqs, n);
   if (rc) return rc;
+  CacheIoParams p{};
   unsigned int blocks = 0;
-  rc = cache_io_grid(n, H, d, &blocks);
+  rc = cache_io_shape(n, H, d, &p, &blocks);
   if (rc) return rc;
   if (blocks == 0) return IAMAP_OK;
   DeviceContext* ctx = device_context();
   if (!ctx) return IAMAP_ERR_CUDA;
-  CacheIoParams p{};
   p.out = static_cast<__nv_bfloat16*>(out);
   p.n = n;
   p.cu = cu;
   p.starts = starts;
   p.num_seqs = num_seqs;
-  p.d = d;
   p.pages = QuantPages{static_cast<const uint8_t*>(codes), static_cast<const __half*>(scales),
                        num_pages, page_table, max_pages, page_size, H};
   p.status = ctx->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (bits == 4)
-    cache_read_kernel<4><<<blocks, kThreads, 0, st>>>(p);
-  else
-    cache_read_kernel<8><<<blocks, kThreads, 0, st>>>(p);
+  if (d == 64) {
+    if (bits == 4) cache_read_kernel<64, 4><<<blocks, kThreads, 0, st>>>(p);
+    else cache_read_kernel<64, 8><<<blocks, kThreads, 0, st>>>(p);
+  } else {
+    if (bits == 4) cache_read_kernel<128, 4><<<blocks, kThreads, 0, st>>>(p);
+    else cache_read_kernel<128, 8><<<blocks, kThreads, 0, st>>>(p);
+  }
   IAMAP_LAUNCH_CHECK("cache_read_kernel");
   return IAMAP_OK;
 }

@@ -154,6 +154,14 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _raw_stream(stream):
+    """The CUDA stream's address as an int (torch's current stream of the current device unless one is
+    given)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
+
+
 def _host_i32(a):
     """Host int32 buffer (numpy array, list or CPU tensor) -> (ctypes pointer, keep-alive)."""
     t = torch.as_tensor(a, dtype=torch.int32).cpu().contiguous()
@@ -526,18 +534,27 @@ def iamap_prefix_lookup(keys, count, key_cu, num_seqs, table_keys, table_vals, c
         _ptr(found), _ptr(hit_blocks), _stream(stream)))
 
 
+# The calls of a decode step are short on the GPU, so their marshalling is kept lean: addresses as plain
+# ints, one ctypes call.
+
 def iamap_cache_write(x, x_stride, n, cu, starts, num_seqs, page_table, max_pages, page_size,
                       num_pages, H, d, bits, codes, scales, stream=None):
-    _check("iamap_cache_write", _lib.iamap_cache_write(
-        _ptr(x), x_stride, n, _ptr(cu), _ptr(starts), num_seqs, _ptr(page_table), max_pages,
-        page_size, num_pages, H, d, bits, _ptr(codes), _ptr(scales), _stream(stream)))
+    rc = _lib.iamap_cache_write(
+        x.data_ptr(), x_stride, n, cu.data_ptr(), starts.data_ptr(), num_seqs,
+        page_table.data_ptr(), max_pages, page_size, num_pages, H, d, bits, codes.data_ptr(),
+        scales.data_ptr(), _raw_stream(stream))
+    if rc:
+        raise IamapError("iamap_cache_write", rc)
 
 
 def iamap_cache_read(codes, scales, num_pages, page_table, max_pages, page_size, cu, starts,
                      num_seqs, n, H, d, bits, out, stream=None):
-    _check("iamap_cache_read", _lib.iamap_cache_read(
-        _ptr(codes), _ptr(scales), num_pages, _ptr(page_table), max_pages, page_size, _ptr(cu),
-        _ptr(starts), num_seqs, n, H, d, bits, _ptr(out), _stream(stream)))
+    rc = _lib.iamap_cache_read(
+        codes.data_ptr(), scales.data_ptr(), num_pages, page_table.data_ptr(), max_pages, page_size,
+        cu.data_ptr(), starts.data_ptr(), num_seqs, n, H, d, bits, out.data_ptr(),
+        _raw_stream(stream))
+    if rc:
+        raise IamapError("iamap_cache_read", rc)
 
 
 def iamap_sender_rows_quant_workspace_bytes(batch, H_s, max_ctx) -> int:
@@ -547,10 +564,12 @@ def iamap_sender_rows_quant_workspace_bytes(batch, H_s, max_ctx) -> int:
 def iamap_sender_rows_quant(q, k_codes, k_scales, num_pages, page_table, max_pages, page_size,
                             ctx_lens, max_ctx, batch, H_s, H_k, d, bits, p_rows, ctx_stride, ws,
                             stream=None):
-    _check("iamap_sender_rows_quant", _lib.iamap_sender_rows_quant(
-        _ptr(q), _ptr(k_codes), _ptr(k_scales), num_pages, _ptr(page_table), max_pages, page_size,
-        _ptr(ctx_lens), max_ctx, batch, H_s, H_k, d, bits, _ptr(p_rows), ctx_stride, _ptr(ws),
-        ws.numel() * ws.element_size(), _stream(stream)))
+    rc = _lib.iamap_sender_rows_quant(
+        q.data_ptr(), k_codes.data_ptr(), k_scales.data_ptr(), num_pages, page_table.data_ptr(),
+        max_pages, page_size, ctx_lens.data_ptr(), max_ctx, batch, H_s, H_k, d, bits,
+        p_rows.data_ptr(), ctx_stride, ws.data_ptr(), ws.nbytes, _raw_stream(stream))
+    if rc:
+        raise IamapError("iamap_sender_rows_quant", rc)
 
 
 def iamap_mapped_av_paged_quant_workspace_bytes(batch, H_r, d_v, max_ctx) -> int:
@@ -560,10 +579,12 @@ def iamap_mapped_av_paged_quant_workspace_bytes(batch, H_r, d_v, max_ctx) -> int
 def iamap_mapped_av_paged_quant(p_rows, ctx_stride, W, v_codes, v_scales, num_pages, page_table,
                                 max_pages, page_size, ctx_lens, max_ctx, batch, H_s, H_r, H_kv,
                                 d_v, bits, out, ws, stream=None):
-    _check("iamap_mapped_av_paged_quant", _lib.iamap_mapped_av_paged_quant(
-        _ptr(p_rows), ctx_stride, _ptr(W), _ptr(v_codes), _ptr(v_scales), num_pages,
-        _ptr(page_table), max_pages, page_size, _ptr(ctx_lens), max_ctx, batch, H_s, H_r, H_kv,
-        d_v, bits, _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    rc = _lib.iamap_mapped_av_paged_quant(
+        p_rows.data_ptr(), ctx_stride, W.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+        num_pages, page_table.data_ptr(), max_pages, page_size, ctx_lens.data_ptr(), max_ctx, batch,
+        H_s, H_r, H_kv, d_v, bits, out.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream))
+    if rc:
+        raise IamapError("iamap_mapped_av_paged_quant", rc)
 
 
 def iamap_attention_paged_quant_workspace_bytes(batch, H_q, d, max_ctx) -> int:
@@ -573,10 +594,13 @@ def iamap_attention_paged_quant_workspace_bytes(batch, H_q, d, max_ctx) -> int:
 def iamap_attention_paged_quant(q, k_codes, k_scales, k_bits, v_codes, v_scales, v_bits, num_pages,
                                 page_table, max_pages, page_size, ctx_lens, max_ctx, batch, H_q,
                                 H_kv, d, out, lse, ws, stream=None):
-    _check("iamap_attention_paged_quant", _lib.iamap_attention_paged_quant(
-        _ptr(q), _ptr(k_codes), _ptr(k_scales), k_bits, _ptr(v_codes), _ptr(v_scales), v_bits,
-        num_pages, _ptr(page_table), max_pages, page_size, _ptr(ctx_lens), max_ctx, batch, H_q,
-        H_kv, d, _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    rc = _lib.iamap_attention_paged_quant(
+        q.data_ptr(), k_codes.data_ptr(), k_scales.data_ptr(), k_bits, v_codes.data_ptr(),
+        v_scales.data_ptr(), v_bits, num_pages, page_table.data_ptr(), max_pages, page_size,
+        ctx_lens.data_ptr(), max_ctx, batch, H_q, H_kv, d, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream))
+    if rc:
+        raise IamapError("iamap_attention_paged_quant", rc)
 
 
 # ------------------------------------------------------------------------------------------------

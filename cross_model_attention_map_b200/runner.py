@@ -181,9 +181,10 @@ class DecodeStep:
 def _expect(name, t, dtype, shape, device):
     """A tensor that the library will read through its address alone: right type, shape, device,
     and packed."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, got %s %s on %s" % (
-            name, dtype, shape, device, t.dtype, tuple(t.shape), t.device))
+    if (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        return
+    raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, got %s %s on %s" % (
+        name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
 
 
 class QuantCache:
@@ -225,39 +226,42 @@ class QuantCache:
         num_seqs = starts.numel()
         _expect("cu", cu, torch.int32, (num_seqs + 1,), self.device)
         _expect("starts", starts, torch.int32, (num_seqs,), self.device)
-        self._table(page_table, num_seqs)
-        return num_seqs
+        return num_seqs, self._table(page_table, num_seqs)
 
     def _table(self, page_table, num_seqs):
-        if self.device.index != torch.cuda.current_device():
+        if self.device.index != torch._C._cuda_getDevice():
             raise ValueError("the cache lies on %s, which is not the current device" % self.device)
-        _expect("page_table", page_table, torch.int32, (num_seqs, page_table.shape[-1]),
-                self.device)
+        shape = page_table.shape
+        if len(shape) != 2:
+            raise ValueError("page_table must be [sequences, max_pages]")
+        _expect("page_table", page_table, torch.int32, (num_seqs, shape[1]), self.device)
+        return shape[1]
 
     def write(self, x, cu, starts, page_table, stream=None):
         """Quantises row cu[s] + i of x as token starts[s] + i of sequence s. x: bf16 [n, H, d] or
         [n, H * d]; its rows may lie further apart than H * d (a slice of a fused projection).
         cu int32 [num_seqs + 1], starts int32 [num_seqs] and page_table int32
         [num_seqs, max_pages] on the device."""
-        num_seqs = self._ranges(cu, starts, page_table)
-        n, width = int(x.shape[0]), self.H * self.d
-        rows = ((width,), (1,)) if x.dim() == 2 else ((self.H, self.d), (self.d, 1))
-        if (x.dtype != torch.bfloat16 or x.device != self.device
-                or tuple(x.shape[1:]) != rows[0] or (n and x.stride()[1:] != rows[1])):
+        num_seqs, max_pages = self._ranges(cu, starts, page_table)
+        shape, stride = x.shape, x.stride()
+        n, width = shape[0], self.H * self.d
+        packed = ((shape[1:] == (width,) and stride[1:] == (1,))
+                  or (shape[1:] == (self.H, self.d) and stride[1:] == (self.d, 1)))
+        if x.dtype is not torch.bfloat16 or x.device != self.device or not (packed or n == 0):
             raise ValueError("x must be bf16 [n, H, d] or [n, H * d] on %s with packed rows"
                              % self.device)
-        C.iamap_cache_write(x, x.stride(0) if n > 1 else width, n, cu, starts, num_seqs,
-                            page_table, page_table.shape[1], self.page_size, self.num_pages,
+        C.iamap_cache_write(x, stride[0] if n > 1 else width, n, cu, starts, num_seqs,
+                            page_table, max_pages, self.page_size, self.num_pages,
                             self.H, self.d, self.bits, self.codes, self.scales, stream)
 
     def read(self, cu, starts, page_table, out, stream=None):
         """Fills row cu[s] + i of out (bf16 [n, H, d]) with token starts[s] + i of sequence s and
         returns out; rows behind the last sequence stay as they are."""
-        num_seqs = self._ranges(cu, starts, page_table)
-        n = int(out.shape[0])
+        num_seqs, max_pages = self._ranges(cu, starts, page_table)
+        n = out.shape[0]
         _expect("out", out, torch.bfloat16, (n, self.H, self.d), self.device)
         C.iamap_cache_read(self.codes, self.scales, self.num_pages, page_table,
-                           page_table.shape[1], self.page_size, cu, starts, num_seqs, n, self.H,
+                           max_pages, self.page_size, cu, starts, num_seqs, n, self.H,
                            self.d, self.bits, out, stream)
         return out
 
@@ -277,12 +281,13 @@ class QuantSenderRows:
         self.rows = torch.empty(batch, H_s, self.ctx_stride, dtype=torch.float32, device=device)
 
     def run(self, q, cache, page_table, ctx_lens, stream=None):
-        _expect("q", q, torch.bfloat16, (self.batch, self.H_s, self.d), self.rows.device)
-        _expect("ctx_lens", ctx_lens, torch.int32, (self.batch,), self.rows.device)
+        dev = self.rows.device
+        _expect("q", q, torch.bfloat16, (self.batch, self.H_s, self.d), dev)
+        _expect("ctx_lens", ctx_lens, torch.int32, (self.batch,), dev)
         _same_cache(cache, self.H_k, self.d)
-        cache._table(page_table, self.batch)
+        max_pages = cache._table(page_table, self.batch)
         C.iamap_sender_rows_quant(q, cache.codes, cache.scales, cache.num_pages, page_table,
-                                  page_table.shape[1], cache.page_size, ctx_lens, self.max_ctx,
+                                  max_pages, cache.page_size, ctx_lens, self.max_ctx,
                                   self.batch, self.H_s, self.H_k, self.d, cache.bits, self.rows,
                                   self.ctx_stride, self.ws, stream)
         return self.rows
@@ -307,9 +312,9 @@ class QuantDecodeStep:
         _expect("W", W, torch.float32, (self.H_r, self.H_s), dev)
         _expect("ctx_lens", ctx_lens, torch.int32, (self.batch,), dev)
         _same_cache(cache, self.H_kv, self.d_v)
-        cache._table(page_table, self.batch)
+        max_pages = cache._table(page_table, self.batch)
         C.iamap_mapped_av_paged_quant(p_rows, self.ctx_stride, W, cache.codes, cache.scales,
-                                      cache.num_pages, page_table, page_table.shape[1],
+                                      cache.num_pages, page_table, max_pages,
                                       cache.page_size, ctx_lens, self.max_ctx, self.batch,
                                       self.H_s, self.H_r, self.H_kv, self.d_v, cache.bits,
                                       self.out, self.ws, stream)
@@ -330,16 +335,17 @@ class QuantAttention:
         self.lse = torch.empty(batch, H_q, dtype=torch.float32, device=device) if want_lse else None
 
     def run(self, q, k_cache, v_cache, page_table, ctx_lens, stream=None):
-        _expect("q", q, torch.bfloat16, (self.batch, self.H_q, self.d), self.out.device)
-        _expect("ctx_lens", ctx_lens, torch.int32, (self.batch,), self.out.device)
+        dev = self.out.device
+        _expect("q", q, torch.bfloat16, (self.batch, self.H_q, self.d), dev)
+        _expect("ctx_lens", ctx_lens, torch.int32, (self.batch,), dev)
         _same_cache(k_cache, self.H_kv, self.d)
         _same_cache(v_cache, self.H_kv, self.d)
-        if (k_cache.num_pages, k_cache.page_size) != (v_cache.num_pages, v_cache.page_size):
+        if k_cache.num_pages != v_cache.num_pages or k_cache.page_size != v_cache.page_size:
             raise ValueError("keys and values must share their pages")
-        k_cache._table(page_table, self.batch)
+        max_pages = k_cache._table(page_table, self.batch)
         C.iamap_attention_paged_quant(q, k_cache.codes, k_cache.scales, k_cache.bits,
                                       v_cache.codes, v_cache.scales, v_cache.bits,
-                                      k_cache.num_pages, page_table, page_table.shape[1],
+                                      k_cache.num_pages, page_table, max_pages,
                                       k_cache.page_size, ctx_lens, self.max_ctx, self.batch,
                                       self.H_q, self.H_kv, self.d, self.out, self.lse, self.ws,
                                       stream)
