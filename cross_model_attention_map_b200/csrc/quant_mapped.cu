@@ -4,20 +4,20 @@
 //
 // Bound by the value bytes (72 a token and head of 128 in 4 bits). A CTA takes a range of tokens of one
 // sequence and up to eight units, a unit being a value head with up to eight of the receiver heads that
-// read it. First the CTA forms w of its receivers and tokens in shared memory (fp32); then each warp
-// streams the tokens of one unit through a ring of copies, 32 at a time.
+// read it. First the CTA forms w of its receivers and tokens in shared memory (fp32 sums); then each warp
+// streams the tokens of one unit through a ring of copies.
 //
 // The product runs on matrix instructions with the codes as one operand (quant_tile.cuh). Its other
 // operand, the weight times the token's scale of the group, has to keep fp32's precision in fp16, so it
-// is held as two parts, hi + lo, in two columns of the same instruction:
+// is held as two parts, high and low, in two columns of the same instruction:
 //
 //   w 2^k = h + l,  P1 = rn(h s),  P2 = rn(l s + (h s - P1))    (h s - P1 is exact in one fma)
 //
-// which leaves an error of 2^-22 relative, or 2^-25 absolute: k brings the largest |w| of the unit's
-// tokens near 2^15, and scales outside [2^-8, 1) are brought under 1 by a power of two of the unit, so
-// nothing overflows and the absolute part is far below the largest products.
-// With one receiver a value head (group 1), the eight columns are the (group of 32, part) pairs, and
-// one operand serves all groups; otherwise they are (receiver, part) and the operand is formed a group.
+// which leaves an error of 2^-22 relative, or 2^-25 absolute: k brings the receiver's largest |w| of the
+// range near 2^14, so the absolute part is far below the largest products. Scales of 2 and more are taken
+// times a power of two of the warp's own (2^-E), found when one comes. With one receiver a value head (group 1),
+// the eight columns are the (group of 32, part) pairs, and one operand serves all groups; otherwise they
+// are (receiver, part) and the operand is formed a group.
 //
 // Partial sums of the ranges go to the workspace; a second kernel adds them in a fixed order.
 #include <algorithm>
@@ -54,9 +54,9 @@ struct MappedParams {
   unsigned int* status;
 };
 
-// Exponent k that brings the largest |w| (bits of a non-negative float) into [2^14, 2^15).
+// Exponent k that brings the largest |w| (bits of a non-negative float) into [2^13, 2^14).
 __device__ __forceinline__ int boost_exp(uint32_t wmax) {
-  return wmax == 0 || wmax >= 0x7f800000u ? 0 : 14 - ((int)(wmax >> 23) - 127);
+  return wmax == 0 || wmax >= 0x7f800000u ? 0 : 13 - ((int)(wmax >> 23) - 127);
 }
 __device__ __forceinline__ float pow2i(int k) {
   // k in [-126, 127] after clamping; larger shifts are made in two steps by the caller
@@ -65,9 +65,10 @@ __device__ __forceinline__ float pow2i(int k) {
 
 template <int D, int BITS>
 struct Ring {
-  static constexpr int kStage = kPair * D * BITS / 8;
-  static constexpr int kStages = kStage <= 2048 ? 3 : 2;
-  static constexpr int kWarp = kChunk * (D / 32) * 2 + kStages * kStage;   // scales and stages
+  static constexpr int kRow = D * BITS / 8 + (D / 32) * 2;
+  // Tiles a step: as many as leave two CTAs an SM two stages a warp.
+  static constexpr int kTiles = kRow <= 72 ? 4 : 2, kTokens = kTiles * kTok, kStages = 2;
+  static constexpr int kWarp = kStages * kTokens * kRow;
 };
 
 // GM 0: group 1; GM 1, 2: up to four, eight receivers a unit.
@@ -75,10 +76,10 @@ template <int D, int BITS, bool ALIGNED, int GM>
 __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedParams p) {
   constexpr int NG = D / 32, R = D * BITS / 8, SB = NG * 2, CT = GM == 2 ? 2 : 1;
   using RB = Ring<D, BITS>;
-  constexpr int ST = RB::kStages;
+  constexpr int ST = RB::kStages, TK = RB::kTokens;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ StreamShared<2, ST> shared[kWarps];
-  __shared__ int up_s[kMaxRecv];
+  __shared__ StreamShared<RB::kTiles, ST> shared[kWarps];
+  __shared__ uint32_t max_s[kMaxRecv];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tid = lane & 3;
 
   int u = blockIdx.x;
@@ -90,47 +91,42 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
   if (chunk >= nchunk) return;
   const int j0 = chunk * kChunk, ntok = min(ctx - j0, kChunk);
 
-  // this warp's unit and tokens: steps of 32 at j0 + 32 (part + parts i)
+  // this warp's unit and tokens: steps of TK at j0 + TK (part + parts i)
   const int unit = slice * p.hs + warp % p.hs, part = warp / p.hs;
   const bool live = unit < p.units;
   const int hk = live ? unit / p.rtiles : 0, rt = unit % p.rtiles;
-  float* w_s = reinterpret_cast<float*>(smem + kWarps * RB::kWarp);
-  const uint32_t scales = smem_u32(smem) + warp * RB::kWarp;   // the unit's scales, step after step
-  Stream<ALIGNED, 2, 1, ST> in;
-  in.init(&p.v, b, hk, j0 + part * kPair, p.parts * kPair, live ? j0 + ntok : 0, p.status,
-          scales + kChunk * SB, &shared[warp]);
+  const int nrj = min(p.rj, p.group - rt * p.rj);            // receivers of this unit
+  Stream<ALIGNED, RB::kTiles, 2, ST> in;
+  in.init(&p.v, b, hk, j0 + part * TK, p.parts * TK, live ? j0 + ntok : 0, p.status,
+          smem_u32(smem) + warp * RB::kWarp, &shared[warp]);
   in.template add<0>(p.v.codes, R);
-  // all scales of the unit's tokens first (a few KB): their largest sets the operand's scale
-  for (int i = 0; i < in.nsteps; ++i) {
-    const uint32_t row = in.rows.at(j0 + (part + p.parts * i) * kPair + lane, p.status);
-    cp_async<SB>(scales + (i * kPair + lane) * SB,
-                 reinterpret_cast<const uint8_t*>(p.v.scales) + (row == kNoRow ? 0 : (uint64_t)row * SB),
-                 row != kNoRow);
-  }
-  cp_async_commit();
+  in.template add<1>(p.v.scales, SB);
 #pragma unroll
   for (int i = 0; i < ST - 1; ++i) in.fill(i);
 
   // the weights of the CTA's receivers: two tokens a thread, eight receivers at a time
   const int recv = p.hs * p.rj;
-  float* W_s = w_s + recv * (kChunk + kPad);               // [H_s][wcols], wcols a multiple of 8
+  uint32_t* w_s = reinterpret_cast<uint32_t*>(smem + kWarps * RB::kWarp);   // [recv][kChunk + kPad]
+  float* W_s = reinterpret_cast<float*>(w_s + recv * (kChunk + kPad));      // [H_s][wcols], wcols a multiple of 8
   const int wcols = (recv + 7) & ~7;
   for (int e = threadIdx.x; e < p.H_s * wcols; e += kThreads) {
     const int s = e / wcols, r = e - s * wcols, un = slice * p.hs + r / p.rj;
-    const int in = (un % p.rtiles) * p.rj + r % p.rj;        // receiver within its value head
-    const bool ok = r < recv && un < p.units && in < p.group;
-    W_s[e] = ok ? __ldg(p.W + ((int64_t)(un / p.rtiles) * p.group + in) * p.H_s + s) : 0.f;
+    const int of = (un % p.rtiles) * p.rj + r % p.rj;        // receiver within its value head
+    const bool ok = r < recv && un < p.units && of < p.group;
+    W_s[e] = ok ? __ldg(p.W + ((int64_t)(un / p.rtiles) * p.group + of) * p.H_s + s) : 0.f;
   }
+  if (threadIdx.x < kMaxRecv) max_s[threadIdx.x] = 0;
   __syncthreads();
   {
     const int t = threadIdx.x;
     const float* row = p.rows + (int64_t)b * p.H_s * p.stride + j0 + t;
     const bool ok0 = t < ntok, ok1 = t + kThreads < ntok;
+#pragma unroll 1
     for (int r0 = 0; r0 < recv; r0 += 8) {
       float a[8], c[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) a[k] = c[k] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
       for (int s = 0; s < p.H_s; ++s) {
         const float x = ok0 ? __ldg(row + (int64_t)s * p.stride) : 0.f;
         const float y = ok1 ? __ldg(row + (int64_t)s * p.stride + kThreads) : 0.f;
@@ -140,64 +136,31 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
 #pragma unroll
         for (int k = 0; k < 8; ++k) a[k] = fmaf(wk[k], x, a[k]), c[k] = fmaf(wk[k], y, c[k]);
       }
+      // a weight times a token that does not exist is no weight, whatever W holds
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (r0 + k < recv) {
-          w_s[(r0 + k) * (kChunk + kPad) + t] = ok0 ? a[k] : 0.f;
-          w_s[(r0 + k) * (kChunk + kPad) + t + kThreads] = ok1 ? c[k] : 0.f;
-        }
-    }
-  }
-  __syncthreads();
-  // each receiver's weights, times the power of two that brings the largest near 2^15, as two fp16 parts
-  // (high part in the low half) in place
-  for (int r = warp; r < recv; r += kWarps) {
-    float* w = w_s + r * (kChunk + kPad);
-    uint32_t m = 0;
-    float v[kChunk / 32];
+      for (int k = 0; k < 8; ++k) {
+        a[k] = ok0 ? a[k] : 0.f;
+        c[k] = ok1 ? c[k] : 0.f;
+        const uint32_t m = __reduce_max_sync(
+            0xffffffffu, max(__float_as_uint(a[k]) & 0x7fffffffu, __float_as_uint(c[k]) & 0x7fffffffu));
+        if (lane == k && r0 + k < recv) atomicMax(&max_s[r0 + k], m);
+      }
+      __syncthreads();
+      // two fp16 parts of w 2^k, the high one in the low half
 #pragma unroll
-    for (int k = 0; k < kChunk / 32; ++k) {
-      v[k] = w[lane + 32 * k];
-      m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
+      for (int k = 0; k < 8; ++k) {
+        if (r0 + k >= recv) break;
+        const int up = boost_exp(max_s[r0 + k]);
+        const float up0 = pow2i(up / 2), up1 = pow2i(up - up / 2);
+        const float x = a[k] * up0 * up1, y = c[k] * up0 * up1;
+        const float hx = __half2float(__float2half_rn(x)), hy = __half2float(__float2half_rn(y));
+        w_s[(r0 + k) * (kChunk + kPad) + t] = pack_f16(hx, x - hx);
+        w_s[(r0 + k) * (kChunk + kPad) + t + kThreads] = pack_f16(hy, y - hy);
+      }
     }
-    m = __reduce_max_sync(0xffffffffu, m);
-    const int up = boost_exp(m);
-    const float up0 = pow2i(up / 2), up1 = pow2i(up - up / 2);
-#pragma unroll
-    for (int k = 0; k < kChunk / 32; ++k) {
-      const float x = v[k] * up0 * up1, h = __half2float(__float2half_rn(x));
-      reinterpret_cast<uint32_t*>(w)[lane + 32 * k] = pack_f16(h, x - h);
-    }
-    if (lane == 0) up_s[r] = up;
   }
   __syncthreads();
 
-  // largest scale of the unit's tokens
-  cp_async_wait<ALIGNED ? 0 : ST - 1>();                     // the scales, started before the ring's copies
-  __syncwarp();
-  const int nrj = min(p.rj, p.group - rt * p.rj);            // receivers of this unit
-  uint32_t smax = 0;
-  for (int e = lane * 4; e < in.nsteps * kPair * SB; e += 128) {
-    const uint32_t v = lds32(scales + e) & 0x7fff7fffu;
-    smax = __vmaxu2(smax, v & ~__vcmpgtu2(v, 0x7bff7bffu));   // infinities and NaN set no scale
-  }
-  smax = max(smax & 0xffffu, smax >> 16);
-  smax = __reduce_max_sync(0xffffffffu, smax);
-  int sdown = 0;
-  if (smax != 0) {
-    const int es = (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)smax))) >> 23) - 127;
-    if (es >= 0 || es < -8) {                                // unusual sizes: scales brought under 1
-      sdown = es + 1;
-      // 2^-sdown in two factors that fp16 has (sdown is in [-23, 16])
-      const uint32_t f0 = pack_f16(pow2i(-(sdown / 2)), pow2i(-(sdown / 2)));
-      const uint32_t f1 = pack_f16(pow2i(-(sdown - sdown / 2)), pow2i(-(sdown - sdown / 2)));
-      for (int e = lane * 4; e < in.nsteps * kPair * SB; e += 128)
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(scales + e),
-                     "r"(hmul2(hmul2(lds32(scales + e), f0), f1))
-                     : "memory");
-      __syncwarp();
-    }
-  }
   // this column's receiver (0 stands in for one that the unit lacks)
   uint32_t wr[CT];
   int kexp[CT];
@@ -205,8 +168,8 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
   for (int c = 0; c < CT; ++c) {
     int r = GM == 0 ? 0 : 4 * c + (gid >> 1);
     r = (warp % p.hs) * p.rj + (r < nrj ? r : 0);
-    wr[c] = smem_u32(w_s + r * (kChunk + kPad) + part * kPair + tid);
-    kexp[c] = up_s[r] - sdown;
+    wr[c] = smem_u32(w_s + r * (kChunk + kPad) + part * TK + tid);
+    kexp[c] = boost_exp(max_s[r]);
   }
 
   float o[CT][2 * NG][4];
@@ -217,69 +180,119 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[c][i][e] = 0.f;
   const bool lo = gid & 1;
+  int E = 0;                                                 // the scales are taken times 2^-E
+  uint32_t down = 0x3c003c00u;                               // 2^-E
 
   for (int i = 0; i < in.nsteps; ++i) {
     in.fill(i + ST - 1);
     uint32_t st;
     const uint32_t* masks;
     if (!in.take(&st, &masks)) break;
-    const uint32_t mask = masks[0];
+    const uint32_t scales = st + TK * R;
+    // a scale of 2 or more (infinite, NaN) in the step
+    const uint2 all = lds64(scales + lane * 8 % (TK * SB));
+    const uint2 all2 = TK * SB > 256 ? lds64(scales + 256 + lane * 8) : make_uint2(0, 0);
+    if (__any_sync(0xffffffffu, (all.x | all.y | all2.x | all2.y) & 0x40004000u)) {
+      uint32_t m = 0;
+      const uint32_t q[4] = {all.x, all.y, all2.x, all2.y};
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      ValueTile<D, BITS> vt;
-      vt.load(st + q * kTok * R);
-      const uint32_t sp = scales + (i * kPair + q * kTok + tid) * SB;   // tokens tid + 4 k
-      uint2 sc[4];
-      if (GM != 0) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sc[k] = lds_scales<NG>(sp + 4 * k * SB);
+      for (int e = 0; e < 4; ++e) {
+        const int t = (lane * 8 % (TK * SB) + 256 * (e >> 1) + 4 * (e & 1)) / SB % TK;   // the word's token
+        if (!((masks[t >> 5] >> (t & 31)) & 1)) continue;
+        const uint32_t v = q[e] & 0x7fff7fffu;
+        m = __vmaxu2(m, v & ~__vcmpgtu2(v, 0x7bff7bffu));     // infinities and NaN set no scale
       }
-      uint32_t hp[CT][2], lp[CT][2];                          // weight pairs, high and low parts
+      m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+      const int e = m < 0x4000u ? 0 : (int)(m >> 10) - 15;    // floor(log2) of the largest scale
+      if (e > E) {
+        const float f = pow2i(E - e);
 #pragma unroll
-      for (int c = 0; c < CT; ++c)
+        for (int c = 0; c < CT; ++c)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t at = wr[c] + (i * p.parts * kPair + q * kTok) * 4 + 32 * h;
-          const uint32_t a = lds32(at), d = lds32(at + 16);
-          hp[c][h] = __byte_perm(a, d, 0x5410);
-          lp[c][h] = __byte_perm(a, d, 0x7632);
-        }
-      if (mask != 0xffffffffu) {
-        // tokens that do not exist: no weight (their scales are 0, their codes may be anything)
-        const uint32_t m = mask >> (q * kTok + tid);
+          for (int k = 0; k < 2 * NG; ++k)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t keep = ((m >> (8 * h)) & 1 ? 0xffffu : 0u) | ((m >> (8 * h + 4)) & 1 ? 0xffff0000u : 0u);
-#pragma unroll
-          for (int c = 0; c < CT; ++c) hp[c][h] &= keep, lp[c][h] &= keep;
-        }
+            for (int z = 0; z < 4; ++z) o[c][k][z] *= f;
+        E = e;
+        down = pack_f16(pow2i(-E), pow2i(-E));
       }
-      auto weight = [&](int c, int h, uint32_t s) {
-        const uint32_t p1 = hmul2(hp[c][h], s);
-        const uint32_t p2 = hfma2(lp[c][h], s, hfma2(hp[c][h], s, p1 ^ 0x80008000u));
-        return lo ? p2 : p1;
-      };
-      uint32_t pb[CT][2];
-      if (GM == 0) {
-        const uint32_t sg = sp + 2 * ((gid >> 1) % NG);       // this column's group
+    }
+#pragma unroll 1
+    for (int h = 0; h < RB::kTiles / 2; ++h) {
+      const uint32_t mask = masks[h];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          pb[0][h] = weight(0, h, __byte_perm(lds16(sg + 8 * h * SB), lds16(sg + (8 * h + 4) * SB), 0x5410));
-      }
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
+      for (int q = 0; q < 2; ++q) {
+        const int tile = 2 * h + q;
+        ValueTile<D, BITS> vt;
+        vt.load(st + tile * kTok * R);
+        const uint32_t sp = scales + (tile * kTok + tid) * SB;           // tokens tid + 4 k
+        uint2 sc[4];
+        uint32_t sg[2];                                      // GM 0: this column's group's, as pairs
         if (GM != 0) {
 #pragma unroll
-          for (int c = 0; c < CT; ++c)
+          for (int k = 0; k < 4; ++k) sc[k] = lds_scales<NG>(sp + 4 * k * SB);
+        } else {
+          const uint32_t at = sp + 2 * ((gid >> 1) % NG);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) pb[c][h] = weight(c, h, scale_pair(sc + 2 * h, g));
+          for (int k = 0; k < 2; ++k)
+            sg[k] = __byte_perm(lds16(at + 8 * k * SB), lds16(at + (8 * k + 4) * SB), 0x5410);
         }
-        uint32_t r[4], t[4];
-        vt.group(g, r, t);
+        uint32_t hp[CT][2], lp[CT][2];                       // weight pairs, high and low parts
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          mma_f16(o[c][2 * g], r[0], r[1], t[0], t[1], pb[c][0], pb[c][1]);
-          mma_f16(o[c][2 * g + 1], r[2], r[3], t[2], t[3], pb[c][0], pb[c][1]);
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t at = wr[c] + (i * p.parts * TK + tile * kTok) * 4 + 32 * k;
+            const uint32_t a = lds32(at), d = lds32(at + 16);
+            hp[c][k] = __byte_perm(a, d, 0x5410);
+            lp[c][k] = __byte_perm(a, d, 0x7632);
+          }
+        if (E != 0) {
+          if (GM == 0) {
+            sg[0] = hmul2(sg[0], down), sg[1] = hmul2(sg[1], down);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc[k] = make_uint2(hmul2(sc[k].x, down), hmul2(sc[k].y, down));
+          }
+        }
+        if (mask != 0xffffffffu) {
+          // tokens that do not exist: no weight and no scale (memory behind them may hold anything)
+          const uint32_t m = mask >> (q * kTok + tid);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t keep =
+                ((m >> (8 * k)) & 1 ? 0xffffu : 0u) | ((m >> (8 * k + 4)) & 1 ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) hp[c][k] &= keep, lp[c][k] &= keep;
+            if (GM == 0) sg[k] &= keep;
+          }
+          if (GM != 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (!((m >> (4 * k)) & 1)) sc[k] = make_uint2(0, 0);
+          }
+        }
+        auto weight = [&](int c, int k, uint32_t s) {
+          const uint32_t p1 = hmul2(hp[c][k], s);
+          const uint32_t p2 = hfma2(lp[c][k], s, hfma2(hp[c][k], s, p1 ^ 0x80008000u));
+          return lo ? p2 : p1;
+        };
+        uint32_t pb[CT][2];
+        if (GM == 0) pb[0][0] = weight(0, 0, sg[0]), pb[0][1] = weight(0, 1, sg[1]);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          if (GM != 0) {
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) pb[c][k] = weight(c, k, scale_pair(sc + 2 * k, g));
+          }
+          uint32_t r[4], t[4];
+          vt.group(g, r, t);
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            mma_f16(o[c][2 * g], r[0], r[1], t[0], t[1], pb[c][0], pb[c][1]);
+            mma_f16(o[c][2 * g + 1], r[2], r[3], t[2], t[3], pb[c][0], pb[c][1]);
+          }
         }
       }
     }
@@ -299,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
     const int r = GM == 0 ? 0 : 4 * c + tid;
-    const int k = __shfl_sync(0xffffffffu, kexp[c], GM == 0 ? 0 : 8 * tid);
+    const int k = __shfl_sync(0xffffffffu, kexp[c], GM == 0 ? 0 : 8 * tid) - E;
     const float dn0 = pow2i(-(k / 2)), dn1 = pow2i(-(k - k / 2));
     if (r >= nrj || !live) continue;
     float* dst = (p.parts > 1 ? o_s + ((part * p.hs + warp % p.hs) * p.rj + r) * D : row_of(unit, r)) +
