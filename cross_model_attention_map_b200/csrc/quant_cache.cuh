@@ -56,6 +56,30 @@ __device__ __forceinline__ int quant_ctx(const int32_t* ctx_lens, int seq, int m
   return c;
 }
 
+// A kernel that follows another of the same call starts while that one drains: what it does before
+// after_previous() may not touch what the earlier kernel writes. The first kernel of a call is launched as
+// usual, so everything before the call is complete when any of its kernels starts.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+template <typename P, typename... A>
+int launch_next(const char* what, void (*kernel)(P, A...), dim3 grid, unsigned int threads, size_t smem,
+                cudaStream_t st, P p, A... a) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, a...);
+  if (e != cudaSuccess)
+    return set_error(IAMAP_ERR_CUDA, "launch of %s failed: %s", what, cudaGetErrorString(e));
+  return IAMAP_OK;
+}
+
 // Host checks of a quantised cache and its page table; IAMAP_OK or an error code.
 int check_quant_pages(const void* codes, const void* scales, int64_t num_pages,
                       const int32_t* page_table, int max_pages, int page_size, int H, int d,

@@ -2,10 +2,13 @@
 //
 //   out[b, r] = sum_{j < ctx[b]} w[r, j] v^[b, j, r / group],  w[r, j] = sum_s W[r, s] p[b, s, j]
 //
-// Bound by the value bytes (72 a token and head of 128 in 4 bits). A CTA takes a range of tokens of one
+// Bound by the value bytes (72 a token and head of 128 in 4 bits). A first kernel forms the weights w (a
+// few per cent of the work) and leaves them in the workspace; then a CTA takes a range of tokens of one
 // sequence and up to eight units, a unit being a value head with up to eight of the receiver heads that
-// read it. First the CTA forms w of its receivers and tokens in shared memory (fp32 sums); then each warp
-// streams the tokens of one unit through a ring of copies.
+// read it, and each warp streams the tokens of one unit with their weights through a ring of copies, 64
+// (or 32) at a time. No barrier stands in the loop. (Weights formed by the CTA for its whole range,
+// between barriers, and by every warp for each step, were slower: 104 and 125 us where this takes @@,
+// grouped ragged in 8 bits.)
 //
 // The product runs on matrix instructions with the codes as one operand (quant_tile.cuh). Its other
 // operand, the weight times the token's scale of the group, has to keep fp32's precision in fp16, so it
@@ -13,13 +16,13 @@
 //
 //   w 2^k = h + l,  P1 = rn(h s),  P2 = rn(l s + (h s - P1))    (h s - P1 is exact in one fma)
 //
-// which leaves an error of 2^-22 relative, or 2^-25 absolute: k brings the receiver's largest |w| of the
-// range near 2^14, so the absolute part is far below the largest products. Scales of 2 and more are taken
-// times a power of two of the warp's own (2^-E), found when one comes. With one receiver a value head (group 1),
-// the eight columns are the (group of 32, part) pairs, and one operand serves all groups; otherwise they
-// are (receiver, part) and the operand is formed a group.
+// which leaves an error of 2^-22 relative, or 2^-25 absolute: the first kernel brings the largest |w| of
+// each receiver and 512 tokens, which is what a range holds, into [2^13, 2^14), so the absolute part is far
+// below the largest products. Scales of 2 and more are taken times a power of two of the warp's own (2^-E), found when one
+// comes. With one receiver a value head (group 1), the eight columns are the (group of 32, part) pairs, and
+// one operand serves all groups; otherwise they are (receiver, part) and the operand is formed a group.
 //
-// Partial sums of the ranges go to the workspace; a second kernel adds them in a fixed order.
+// Partial sums of the ranges go to the workspace; a third kernel adds them in a fixed order.
 #include <algorithm>
 
 #include "internal.h"
@@ -32,9 +35,8 @@ using namespace qt;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kChunk = 512;          // tokens a CTA, two a thread
-constexpr int kMaxRecv = 16;         // receivers a CTA
-constexpr int kPad = 4;              // floats between the receivers' weight rows
+constexpr int kBlock = 32;           // tokens of one record of weights: RJ receivers' as (high, low) pairs
+constexpr int kChunk = 512;          // tokens of a range
 
 struct MappedParams {
   const float* rows;                 // [batch, H_s, stride]
@@ -50,46 +52,108 @@ struct MappedParams {
   int slices;                        // CTAs a range
   int chunks;                        // ranges of max_ctx tokens
   float* out;                        // [batch, H_r, d]
+  uint8_t* records;                  // [batch][units][blocks] records of weights
+  int* powers;                       // [batch][units][chunks][RJ]: the powers of two of a range's weights
   float* partial;                    // [batch][chunks][H_r][d]
   unsigned int* status;
 };
 
-// Exponent k that brings the largest |w| (bits of a non-negative float) into [2^13, 2^14).
-__device__ __forceinline__ int boost_exp(uint32_t wmax) {
-  return wmax == 0 || wmax >= 0x7f800000u ? 0 : 13 - ((int)(wmax >> 23) - 127);
-}
+// 2^k for k in [-126, 127], clamped to it; larger shifts are made in two steps by the caller.
 __device__ __forceinline__ float pow2i(int k) {
-  // k in [-126, 127] after clamping; larger shifts are made in two steps by the caller
   return __uint_as_float((uint32_t)(min(max(k, -126), 127) + 127) << 23);
 }
+// The weights: a CTA a range of tokens for eight receivers, two tokens a thread.
+constexpr int kWeightThreads = kChunk / 2;
+template <int RJ>
+__global__ void __launch_bounds__(kWeightThreads) quant_weights_kernel(const MappedParams p) {
+  constexpr int UN = 8 / RJ;                                 // units a CTA
+  extern __shared__ float W_s[];                             // [H_s][8]
+  __shared__ uint32_t max_s[8];
+  let_next_start();
+  const int lane = threadIdx.x & 31, b = blockIdx.y, chunk = blockIdx.z, u0 = blockIdx.x * UN;
+  const int ctx = quant_ctx(p.ctx_lens, b, p.max_ctx, p.status);
+  if (chunk * kChunk >= ctx) return;
+  {
+    const int k = threadIdx.x & 7, un = u0 + k / RJ, of = un % p.rtiles * p.rj + k % RJ;
+    const bool ok = un < p.units && k % RJ < p.rj && of < p.group;
+    const float* src = p.W + ((int64_t)(un / p.rtiles) * p.group + of) * p.H_s;
+    for (int s = threadIdx.x >> 3; s < p.H_s; s += kWeightThreads / 8) W_s[s * 8 + k] = ok ? __ldg(src + s) : 0.f;
+  }
+  if (threadIdx.x < 8) max_s[threadIdx.x] = 0;
+  __syncthreads();
+  const int j = chunk * kChunk + threadIdx.x;
+  const bool there[2] = {j < ctx, j + kWeightThreads < ctx};
+  const float* row = p.rows + (int64_t)b * p.H_s * p.stride + j;
+  float w[2][8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[0][k] = w[1][k] = 0.f;
+#pragma unroll 8
+  for (int s = 0; s < p.H_s; ++s, row += p.stride) {
+    const float x = there[0] ? __ldg(row) : 0.f, y = there[1] ? __ldg(row + kWeightThreads) : 0.f;
+    const float4 f0 = *reinterpret_cast<const float4*>(W_s + s * 8);
+    const float4 f1 = *reinterpret_cast<const float4*>(W_s + s * 8 + 4);
+    const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[0][k] = fmaf(f[k], x, w[0][k]), w[1][k] = fmaf(f[k], y, w[1][k]);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    // a weight of a token that does not exist is 0, whatever W holds
+    w[0][k] = there[0] ? w[0][k] : 0.f;
+    w[1][k] = there[1] ? w[1][k] : 0.f;
+    const uint32_t m = __reduce_max_sync(0xffffffffu, max(__float_as_uint(w[0][k]) & 0x7fffffffu,
+                                                          __float_as_uint(w[1][k]) & 0x7fffffffu));
+    if (lane == k) atomicMax(&max_s[k], m);
+  }
+  __syncthreads();
+  const int n = p.chunks * (kChunk / kBlock), block = chunk * (kChunk / kBlock) + (threadIdx.x >> 5);
+  uint32_t* rec = reinterpret_cast<uint32_t*>(p.records) + (((int64_t)b * p.units + u0) * n + block) * (RJ * kBlock);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (u0 + k / RJ >= p.units) break;
+    // infinities and NaN stay what they are
+    const uint32_t m = max_s[k];
+    const int up = m == 0 || m >= 0x7f800000u ? 0 : min(13 - ((int)(m >> 23) - 127), 126);
+    const float f = pow2i(up);
+    uint32_t* to = rec + (int64_t)(k / RJ) * n * (RJ * kBlock) + k % RJ * kBlock + lane;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float x = w[h][k] * f, high = __half2float(__float2half_rn(x));
+      to[h * (kWeightThreads / kBlock) * (RJ * kBlock)] = pack_f16(high, x - high);
+    }
+    if (threadIdx.x == k)
+      p.powers[(((int64_t)b * p.units + u0 + k / RJ) * p.chunks + chunk) * RJ + k % RJ] = up;
+  }
+}
 
-template <int D, int BITS>
+template <int D, int BITS, int RJ>
 struct Ring {
   static constexpr int kRow = D * BITS / 8 + (D / 32) * 2;
   // Tiles a step: as many as leave two CTAs an SM two stages a warp.
   static constexpr int kTiles = kRow <= 72 ? 4 : 2, kTokens = kTiles * kTok, kStages = 2;
-  static constexpr int kWarp = kStages * kTokens * kRow;
+  static constexpr int kExtra = kTokens * RJ * 4;          // weights a step
+  static constexpr int kWarp = kStages * (kTokens * kRow + kExtra);
 };
 
 // GM 0: group 1; GM 1, 2: up to four, eight receivers a unit.
 template <int D, int BITS, bool ALIGNED, int GM>
-__global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedParams p) {
+__global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams p) {
   constexpr int NG = D / 32, R = D * BITS / 8, SB = NG * 2, CT = GM == 2 ? 2 : 1;
-  using RB = Ring<D, BITS>;
-  constexpr int ST = RB::kStages, TK = RB::kTokens;
+  constexpr int RJ = GM == 0 ? 1 : 4 * GM;
+  using RB = Ring<D, BITS, RJ>;
+  constexpr int ST = RB::kStages, TK = RB::kTokens, REC = kBlock * RJ * 4;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ StreamShared<RB::kTiles, ST> shared[kWarps];
-  __shared__ uint32_t max_s[kMaxRecv];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tid = lane & 3;
 
+  let_next_start();
   int u = blockIdx.x;
   const int slice = u % p.slices;
   u /= p.slices;
   const int b = u % p.batch, chunk = u / p.batch;
   const int ctx = quant_ctx(p.ctx_lens, b, p.max_ctx, p.status);
-  const int nchunk = max(1, (ctx + kChunk - 1) / kChunk);
-  if (chunk >= nchunk) return;
-  const int j0 = chunk * kChunk, ntok = min(ctx - j0, kChunk);
+  const int j0 = chunk * kChunk, j1 = min(ctx, j0 + kChunk);
+  if (j0 >= j1 && chunk > 0) return;
 
   // this warp's unit and tokens: steps of TK at j0 + TK (part + parts i)
   const int unit = slice * p.hs + warp % p.hs, part = warp / p.hs;
@@ -97,80 +161,15 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
   const int hk = live ? unit / p.rtiles : 0, rt = unit % p.rtiles;
   const int nrj = min(p.rj, p.group - rt * p.rj);            // receivers of this unit
   Stream<ALIGNED, RB::kTiles, 2, ST> in;
-  in.init(&p.v, b, hk, j0 + part * TK, p.parts * TK, live ? j0 + ntok : 0, p.status,
+  in.init(&p.v, b, hk, j0 + part * TK, p.parts * TK, live ? j1 : 0, p.status,
           smem_u32(smem) + warp * RB::kWarp, &shared[warp]);
   in.template add<0>(p.v.codes, R);
   in.template add<1>(p.v.scales, SB);
+  in.add_extra(p.records + (((int64_t)b * p.units + (live ? unit : 0)) * p.chunks * kChunk + in.first) * (RJ * 4),
+               RB::kExtra, in.step * (RJ * 4));
+  after_previous();                                          // the weights
 #pragma unroll
   for (int i = 0; i < ST - 1; ++i) in.fill(i);
-
-  // the weights of the CTA's receivers: two tokens a thread, eight receivers at a time
-  const int recv = p.hs * p.rj;
-  uint32_t* w_s = reinterpret_cast<uint32_t*>(smem + kWarps * RB::kWarp);   // [recv][kChunk + kPad]
-  float* W_s = reinterpret_cast<float*>(w_s + recv * (kChunk + kPad));      // [H_s][wcols], wcols a multiple of 8
-  const int wcols = (recv + 7) & ~7;
-  for (int e = threadIdx.x; e < p.H_s * wcols; e += kThreads) {
-    const int s = e / wcols, r = e - s * wcols, un = slice * p.hs + r / p.rj;
-    const int of = (un % p.rtiles) * p.rj + r % p.rj;        // receiver within its value head
-    const bool ok = r < recv && un < p.units && of < p.group;
-    W_s[e] = ok ? __ldg(p.W + ((int64_t)(un / p.rtiles) * p.group + of) * p.H_s + s) : 0.f;
-  }
-  if (threadIdx.x < kMaxRecv) max_s[threadIdx.x] = 0;
-  __syncthreads();
-  {
-    const int t = threadIdx.x;
-    const float* row = p.rows + (int64_t)b * p.H_s * p.stride + j0 + t;
-    const bool ok0 = t < ntok, ok1 = t + kThreads < ntok;
-#pragma unroll 1
-    for (int r0 = 0; r0 < recv; r0 += 8) {
-      float a[8], c[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) a[k] = c[k] = 0.f;
-#pragma unroll 8
-      for (int s = 0; s < p.H_s; ++s) {
-        const float x = ok0 ? __ldg(row + (int64_t)s * p.stride) : 0.f;
-        const float y = ok1 ? __ldg(row + (int64_t)s * p.stride + kThreads) : 0.f;
-        const float4 u0 = *reinterpret_cast<const float4*>(W_s + s * wcols + r0);
-        const float4 u1 = *reinterpret_cast<const float4*>(W_s + s * wcols + r0 + 4);
-        const float wk[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) a[k] = fmaf(wk[k], x, a[k]), c[k] = fmaf(wk[k], y, c[k]);
-      }
-      // a weight times a token that does not exist is no weight, whatever W holds
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        a[k] = ok0 ? a[k] : 0.f;
-        c[k] = ok1 ? c[k] : 0.f;
-        const uint32_t m = __reduce_max_sync(
-            0xffffffffu, max(__float_as_uint(a[k]) & 0x7fffffffu, __float_as_uint(c[k]) & 0x7fffffffu));
-        if (lane == k && r0 + k < recv) atomicMax(&max_s[r0 + k], m);
-      }
-      __syncthreads();
-      // two fp16 parts of w 2^k, the high one in the low half
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (r0 + k >= recv) break;
-        const int up = boost_exp(max_s[r0 + k]);
-        const float up0 = pow2i(up / 2), up1 = pow2i(up - up / 2);
-        const float x = a[k] * up0 * up1, y = c[k] * up0 * up1;
-        const float hx = __half2float(__float2half_rn(x)), hy = __half2float(__float2half_rn(y));
-        w_s[(r0 + k) * (kChunk + kPad) + t] = pack_f16(hx, x - hx);
-        w_s[(r0 + k) * (kChunk + kPad) + t + kThreads] = pack_f16(hy, y - hy);
-      }
-    }
-  }
-  __syncthreads();
-
-  // this column's receiver (0 stands in for one that the unit lacks)
-  uint32_t wr[CT];
-  int kexp[CT];
-#pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    int r = GM == 0 ? 0 : 4 * c + (gid >> 1);
-    r = (warp % p.hs) * p.rj + (r < nrj ? r : 0);
-    wr[c] = smem_u32(w_s + r * (kChunk + kPad) + part * TK + tid);
-    kexp[c] = boost_exp(max_s[r]);
-  }
 
   float o[CT][2 * NG][4];
 #pragma unroll
@@ -179,7 +178,10 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
     for (int i = 0; i < 2 * NG; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[c][i][e] = 0.f;
+  // The operand of a column is rn(l' s + (h' s - rn(h' s))): a low column has h' = h, l' = l, a high one
+  // h' = 0, l' = h.
   const bool lo = gid & 1;
+  const uint32_t own = lo ? 0x3c003c00u : 0u, take_l = lo ? 0x7632u : 0x5410u;
   int E = 0;                                                 // the scales are taken times 2^-E
   uint32_t down = 0x3c003c00u;                               // 2^-E
 
@@ -189,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
     const uint32_t* masks;
     if (!in.take(&st, &masks)) break;
     const uint32_t scales = st + TK * R;
+    const uint32_t weights = scales + TK * SB + (GM == 0 ? 0 : gid >> 1) * (kBlock * 4) + tid * 4;
     // a scale of 2 or more (infinite, NaN) in the step
     const uint2 all = lds64(scales + lane * 8 % (TK * SB));
     const uint2 all2 = TK * SB > 256 ? lds64(scales + 256 + lane * 8) : make_uint2(0, 0);
@@ -241,10 +244,10 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
         for (int c = 0; c < CT; ++c)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint32_t at = wr[c] + (i * p.parts * TK + tile * kTok) * 4 + 32 * k;
+            const uint32_t at = weights + h * REC + c * (4 * kBlock * 4) + q * kTok * 4 + 32 * k;
             const uint32_t a = lds32(at), d = lds32(at + 16);
-            hp[c][k] = __byte_perm(a, d, 0x5410);
-            lp[c][k] = __byte_perm(a, d, 0x7632);
+            hp[c][k] = hmul2(__byte_perm(a, d, 0x5410), own);
+            lp[c][k] = __byte_perm(a, d, take_l);
           }
         if (E != 0) {
           if (GM == 0) {
@@ -272,9 +275,8 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
           }
         }
         auto weight = [&](int c, int k, uint32_t s) {
-          const uint32_t p1 = hmul2(hp[c][k], s);
-          const uint32_t p2 = hfma2(lp[c][k], s, hfma2(hp[c][k], s, p1 ^ 0x80008000u));
-          return lo ? p2 : p1;
+          const uint32_t minus = hmul2(hp[c][k] ^ 0x80008000u, s);
+          return hfma2(lp[c][k], s, hfma2(hp[c][k], s, minus));
         };
         uint32_t pb[CT][2];
         if (GM == 0) pb[0][0] = weight(0, 0, sg[0]), pb[0][1] = weight(0, 1, sg[1]);
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
   if (!ALIGNED) cp_async_wait<0>();
 
   // columns 2 tid, 2 tid + 1 are the two parts of receiver tid (GM 0: of group tid)
-  const bool direct = nchunk == 1;
+  const bool direct = ctx <= kChunk;
   float* o_s = reinterpret_cast<float*>(smem);               // [part][unit of the CTA][rj][D]
   if (p.parts > 1) __syncthreads();                          // the rings are free
   auto row_of = [&](int un, int r) {                         // where a receiver's sums go
@@ -312,9 +314,9 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
     const int r = GM == 0 ? 0 : 4 * c + tid;
-    const int k = __shfl_sync(0xffffffffu, kexp[c], GM == 0 ? 0 : 8 * tid) - E;
-    const float dn0 = pow2i(-(k / 2)), dn1 = pow2i(-(k - k / 2));
     if (r >= nrj || !live) continue;
+    const int k = j0 < j1 ? p.powers[(((int64_t)b * p.units + unit) * p.chunks + chunk) * RJ + r] - E : 0;
+    const float dn0 = pow2i(-(k / 2)), dn1 = pow2i(-(k - k / 2));
     float* dst = (p.parts > 1 ? o_s + ((part * p.hs + warp % p.hs) * p.rj + r) * D : row_of(unit, r)) +
                  4 * gid;
 #pragma unroll
@@ -342,50 +344,76 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(const MappedP
   }
 }
 
-__global__ void __launch_bounds__(256) quant_mapped_join_kernel(const MappedParams p, int d) {
+// Adds the ranges of 128 output elements: eight warps take a range each in turn.
+__global__ void __launch_bounds__(256) quant_mapped_join_kernel(MappedParams p, int d) {
   const int E = p.H_r * d;
-  const int b = blockIdx.y, e = (blockIdx.x * 256 + threadIdx.x) * 4;
-  if (e >= E) return;
+  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e = blockIdx.x * 128 + lane * 4;
   const int ctx = min(max(p.ctx_lens[b], 0), p.max_ctx);
+  after_previous();
   const int n = (ctx + kChunk - 1) / kChunk;
   if (n <= 1) return;
-  const float* src = p.partial + (int64_t)b * p.chunks * E + e;
+  __shared__ __align__(16) float a_s[8][128];
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (e < E) {
+    const float* src = p.partial + (int64_t)b * p.chunks * E + e;
 #pragma unroll 4
-  for (int c = 0; c < n; ++c) {
-    const float4 x = *reinterpret_cast<const float4*>(src + (int64_t)c * E);
-    a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+    for (int c = warp; c < n; c += 8) {
+      const float4 x = *reinterpret_cast<const float4*>(src + (int64_t)c * E);
+      a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+    }
   }
-  *reinterpret_cast<float4*>(p.out + (int64_t)b * E + e) = a;
+  *reinterpret_cast<float4*>(&a_s[warp][lane * 4]) = a;
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t >= 128 || blockIdx.x * 128 + t >= E) return;
+  float sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sum += a_s[k][t];
+  p.out[(int64_t)b * E + blockIdx.x * 128 + t] = sum;
 }
 
-// Units and their place in a CTA for `group` receivers a value head.
-void mapped_shape(int H_kv, int group, int max_ctx, MappedParams* p) {
+// Units and their place in a CTA for `group` receivers a value head, and the workspace: records, powers
+// from *powers_at, partial sums from *partial_at.
+size_t mapped_shape(int batch, int H_kv, int group, int d, int max_ctx, MappedParams* p,
+                    size_t* powers_at, size_t* partial_at) {
   p->group = group;
   p->rj = std::min(group, 8);
   p->rtiles = (group + p->rj - 1) / p->rj;
   p->units = H_kv * p->rtiles;
-  // at most kMaxRecv receivers a CTA keep their weights in 33 KB, so that two CTAs fit an SM
   p->hs = 1;
-  while (p->hs * 2 <= std::min(p->units, kWarps) && p->hs * 2 * p->rj <= kMaxRecv) p->hs *= 2;
+  while (p->hs * 2 <= std::min(p->units, kWarps)) p->hs *= 2;
   p->parts = kWarps / p->hs;
   p->slices = (p->units + p->hs - 1) / p->hs;
   p->chunks = std::max(1, (max_ctx + kChunk - 1) / kChunk);
+  const size_t rj = p->rj == 1 ? 1 : p->rj <= 4 ? 4 : 8, ranges = (size_t)batch * p->units * p->chunks;
+  *powers_at = ranges * kChunk * rj * 4;
+  *partial_at = *powers_at + (ranges * rj * 4 + 255) / 256 * 256;
+  return *partial_at +
+         (p->chunks > 1 ? sizeof(float) * batch * p->chunks * H_kv * group * (size_t)d : 0);
+}
+
+template <int RJ>
+int launch_weights(const MappedParams& p, cudaStream_t st) {
+  const dim3 grid((p.units + 8 / RJ - 1) / (8 / RJ), p.batch, p.chunks);
+  quant_weights_kernel<RJ><<<grid, kWeightThreads, p.H_s * 8 * sizeof(float), st>>>(p);
+  IAMAP_LAUNCH_CHECK("quant_weights_kernel");
+  return IAMAP_OK;
 }
 
 template <int D, int BITS, bool ALIGNED, int GM>
 int launch(const MappedParams& p, unsigned int blocks, cudaStream_t st) {
-  const int bytes = kWarps * Ring<D, BITS>::kWarp +
-                    p.hs * p.rj * (kChunk + kPad) * 4 + p.H_s * ((p.hs * p.rj + 7) & ~7) * 4;
+  constexpr int RJ = GM == 0 ? 1 : 4 * GM;
+  int rc = launch_weights<RJ>(p, st);
+  if (rc) return rc;
+  const int bytes = std::max(kWarps * Ring<D, BITS, RJ>::kWarp, p.parts > 1 ? kWarps * p.rj * D * 4 : 0);
   IAMAP_CUDA_CHECK(cudaFuncSetAttribute(quant_mapped_kernel<D, BITS, ALIGNED, GM>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-  quant_mapped_kernel<D, BITS, ALIGNED, GM><<<blocks, kThreads, bytes, st>>>(p);
-  IAMAP_LAUNCH_CHECK("quant_mapped_kernel");
-  if (p.chunks > 1) {
-    quant_mapped_join_kernel<<<dim3((p.H_r * D / 4 + 255) / 256, p.batch), 256, 0, st>>>(p, D);
-    IAMAP_LAUNCH_CHECK("quant_mapped_join_kernel");
-  }
-  return IAMAP_OK;
+  rc = launch_next("quant_mapped_kernel", quant_mapped_kernel<D, BITS, ALIGNED, GM>, dim3(blocks), kThreads,
+                   bytes, st, p);
+  if (rc || p.chunks == 1) return rc;
+  return launch_next("quant_mapped_join_kernel", quant_mapped_join_kernel,
+                     dim3((p.H_r * D + 127) / 128, p.batch), 256, 0, st, p, D);
 }
 template <int D, int BITS>
 int launch_d(const MappedParams& p, unsigned int blocks, cudaStream_t st) {
@@ -405,8 +433,15 @@ using namespace iamap;
 extern "C" size_t iamap_mapped_av_paged_quant_workspace_bytes(int batch, int H_r, int d_v,
                                                               int max_ctx) {
   if (batch < 1 || H_r < 1 || d_v < 1 || max_ctx < 0) return 0;
-  const size_t chunks = std::max(1, (max_ctx + kChunk - 1) / kChunk);
-  return chunks > 1 ? sizeof(float) * batch * chunks * H_r * d_v : 256;
+  // the most that any grouping of the H_r heads needs
+  size_t most = 256;
+  for (int group = 1; group <= H_r; ++group) {
+    if (H_r % group != 0) continue;
+    MappedParams p{};
+    size_t a, b;
+    most = std::max(most, mapped_shape(batch, H_r / group, group, d_v, max_ctx, &p, &a, &b));
+  }
+  return most;
 }
 
 extern "C" int iamap_mapped_av_paged_quant(const float* p_rows, int ctx_stride, const float* W,
@@ -433,14 +468,14 @@ extern "C" int iamap_mapped_av_paged_quant(const float* p_rows, int ctx_stride, 
   if (ctx_stride < 1 || ctx_stride < max_ctx)
     return set_error(IAMAP_ERR_INVALID_ARG, "ctx_stride=%d is below max_ctx=%d", ctx_stride, max_ctx);
   MappedParams p{};
-  mapped_shape(H_kv, H_r / H_kv, max_ctx, &p);
-  const size_t need = p.chunks > 1 ? sizeof(float) * batch * p.chunks * H_r * d_v : 1;
+  size_t powers_at = 0, partial_at = 0;
+  const size_t need = mapped_shape(batch, H_kv, H_r / H_kv, d_v, max_ctx, &p, &powers_at, &partial_at);
   if (!ws || ws_bytes < need)
     return set_error(IAMAP_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws_bytes);
   if ((reinterpret_cast<uintptr_t>(ws) & 15u) != 0)
     return set_error(IAMAP_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   const int64_t blocks = (int64_t)p.chunks * batch * p.slices;
-  if (blocks > 0x7fffffff)
+  if (blocks > 0x7fffffff || p.chunks > 65535)
     return set_error(IAMAP_ERR_UNSUPPORTED, "batch times heads times max_ctx is too large");
   DeviceContext* ctx = device_context();
   if (!ctx) return IAMAP_ERR_CUDA;
@@ -455,7 +490,9 @@ extern "C" int iamap_mapped_av_paged_quant(const float* p_rows, int ctx_stride, 
   p.H_s = H_s;
   p.H_r = H_r;
   p.out = out;
-  p.partial = static_cast<float*>(ws);
+  p.records = static_cast<uint8_t*>(ws);
+  p.powers = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + powers_at);
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + partial_at);
   p.status = ctx->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (d_v == 64)

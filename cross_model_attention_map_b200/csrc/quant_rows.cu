@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(kThreads, 5) quant_rows_kernel(const RowsParam
   __shared__ StreamShared<2, ST> shared[kWarps];
   __shared__ float2 ml_s[kWarps][kHeads];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tid = lane & 3;
+  let_next_start();
   const int hk = blockIdx.x / p.htiles, ht = blockIdx.x - hk * p.htiles, b = blockIdx.y, split = blockIdx.z;
   const int ctx = quant_ctx(p.ctx_lens, b, p.max_ctx, p.status);
   const int j0 = split * p.chunk, j1 = min(ctx, j0 + p.chunk);
@@ -133,12 +134,13 @@ __global__ void __launch_bounds__(kThreads, 5) quant_rows_kernel(const RowsParam
 }
 
 constexpr int kNormTokens = 2048;    // tokens a CTA of the second kernel
-__global__ void __launch_bounds__(256) quant_rows_norm_kernel(const RowsParams p, int parts) {
+__global__ void __launch_bounds__(256) quant_rows_norm_kernel(RowsParams p, int parts) {
   const int part = blockIdx.x % parts;
   const int64_t r = blockIdx.x / parts;                    // row b * Hq + h
   const int ctx = min(max(p.ctx_lens[r / p.Hq], 0), p.max_ctx);
   const int n = (ctx + p.chunk - 1) / p.chunk;
   const float2* ml = p.ml + r * p.splits;
+  after_previous();
   __shared__ float lse_s;
   if (threadIdx.x < 32) {
     float m = kNoRef, z = 0.f;
@@ -180,9 +182,8 @@ int launch_d(const RowsParams& p, int bits, cudaStream_t st) {
   }
   IAMAP_LAUNCH_CHECK("quant_rows_kernel");
   const int parts = (p.stride + kNormTokens - 1) / kNormTokens;
-  quant_rows_norm_kernel<<<(unsigned int)((int64_t)p.batch * p.Hq * parts), 256, 0, st>>>(p, parts);
-  IAMAP_LAUNCH_CHECK("quant_rows_norm_kernel");
-  return IAMAP_OK;
+  return launch_next("quant_rows_norm_kernel", quant_rows_norm_kernel,
+                     dim3((unsigned int)((int64_t)p.batch * p.Hq * parts)), 256, 0, st, p, parts);
 }
 
 }  // namespace

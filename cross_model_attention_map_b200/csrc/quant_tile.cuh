@@ -326,11 +326,14 @@ struct StreamShared {
 // row is copied by itself in pieces of 16 (codes) or 4 or 8 (scales) bytes, and tokens that do not exist
 // are zeros.
 //
+// A further array without pages may come with them: `extra_bytes` a step from one run of memory, after the
+// others in the stage.
+//
 // Page indices: ALIGNED, lane l looks up tile l of the next 32; otherwise lane l looks up token l of
 // each 32 of a step.
 template <bool ALIGNED, int TILES, int ARRAYS, int STAGES>
 struct Stream {
-  static_assert(TILES * ARRAYS <= 32 && TILES % 2 == 0 && 32 % TILES == 0, "one bulk copy a lane");
+  static_assert(TILES * ARRAYS < 32 && TILES % 2 == 0 && 32 % TILES == 0, "one bulk copy a lane");
   static constexpr int kTokens = TILES * kTok;
   QuantRow rows;
   unsigned int* status;
@@ -346,6 +349,8 @@ struct Stream {
   // all arrays (otherwise)
   const uint8_t* pool[ARRAYS];
   uint32_t row_bytes[ARRAYS];
+  const uint8_t* extra;            // step i's: extra + i * extra_step
+  uint32_t extra_bytes, extra_step;
 
   // Step i is tokens first + i * step .. + kTokens of the sequence, below `end`.
   __device__ __forceinline__ void init(const QuantPages* pages, int seq, int head, int first_,
@@ -355,7 +360,7 @@ struct Stream {
     first = first_, step = step_, status = st, sh = shared, ring = ring_;
     nsteps = end > first ? (end - first + step - 1) / step : 0;
     s_in = s_out = 0, parity = 0, stage_bytes = tile_bytes = 0, good = held = 0;
-    src = nullptr, mul = dst = 0;
+    src = extra = nullptr, mul = dst = extra_bytes = extra_step = 0;
     const int lane = threadIdx.x & 31;
     if (ALIGNED) {
       if (lane < STAGES) tc::mbar_init(smem_u32(&sh->full[lane]), 1);
@@ -382,6 +387,14 @@ struct Stream {
     tile_bytes += kTok * bytes;
   }
 
+  // The array without pages, after the others (16-byte aligned, multiples of 16 bytes).
+  __device__ __forceinline__ void add_extra(const void* base, uint32_t bytes, uint32_t step_bytes) {
+    extra = static_cast<const uint8_t*>(base);
+    extra_bytes = bytes, extra_step = step_bytes;
+    if ((threadIdx.x & 31) == TILES * ARRAYS) dst = stage_bytes;
+    stage_bytes += bytes;
+  }
+
   // Starts step i (called for i = 0, 1, ... by the whole warp; nothing past the last step). Steps
   // 0 .. STAGES - 2 are started first; then step i + STAGES - 1 is started before step i is taken, into
   // the stage that step i - 1 left (the warp has met since its last read).
@@ -398,24 +411,31 @@ struct Stream {
         }
         const uint32_t row = __shfl_sync(0xffffffffu, held, k + lane / ARRAYS % TILES);
         const uint32_t bar = smem_u32(&sh->full[s_in]);
-        if (lane < TILES * ARRAYS && row != kNoRow)
+        const bool linear = lane == TILES * ARRAYS && extra_bytes != 0;
+        if ((lane < TILES * ARRAYS && row != kNoRow) || linear)
           asm volatile(
               "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                   stage + dst),
-              "l"(src + (uint64_t)row * mul), "r"(mul * kTok), "r"(bar)
+              "l"(linear ? extra + (uint64_t)i * extra_step : src + (uint64_t)row * mul),
+              "r"(linear ? extra_bytes : mul * kTok), "r"(bar)
               : "memory");
-        if (lane == 0) {
-          const uint32_t g = good >> k;
-          const int left = rows.end - (first + i * step);
-#pragma unroll
-          for (int h = 0; h < TILES / 2; ++h) {
-            uint32_t m = (g >> (2 * h) & 1 ? 0xffffu : 0u) | (g >> (2 * h) & 2 ? 0xffff0000u : 0u);
-            if (left < (h + 1) * kPair) m &= left <= h * kPair ? 0u : (1u << (left - h * kPair)) - 1u;
-            sh->mask[s_in][h] = m;
+        const uint32_t g = good >> k & ((1u << TILES) - 1u);
+        const int left = rows.end - (first + i * step);
+        uint32_t bytes = tile_bytes * TILES;
+        if (g != (1u << TILES) - 1u || left < kTokens) {
+          bytes = tile_bytes * __popc(g);
+          if (lane < TILES / 2) {
+            uint32_t m = (g >> (2 * lane) & 1 ? 0xffffu : 0u) | (g >> (2 * lane) & 2 ? 0xffff0000u : 0u);
+            const int here = left - lane * kPair;
+            if (here < kPair) m &= here <= 0 ? 0u : (1u << here) - 1u;
+            sh->mask[s_in][lane] = m;
           }
-          // the arrival completes the phase once these bytes have come, before or after it
-          tc::mbar_expect_tx(bar, tile_bytes * __popc(g & ((1u << TILES) - 1u)));
+          __syncwarp();
+        } else if (lane < TILES / 2) {
+          sh->mask[s_in][lane] = 0xffffffffu;
         }
+        // the arrival completes the phase once these bytes have come, before or after it
+        if (lane == 0) tc::mbar_expect_tx(bar, bytes + extra_bytes);
         __syncwarp();
       } else {
 #pragma unroll 1
@@ -442,6 +462,8 @@ struct Stream {
           const uint32_t m = __ballot_sync(0xffffffffu, row != kNoRow);
           if (lane == 0) sh->mask[s_in][h] = m;
         }
+        for (uint32_t at = lane * 16; at < extra_bytes; at += 512)
+          cp_async<16>(stage + stage_bytes - extra_bytes + at, extra + (uint64_t)i * extra_step + at, true);
         __syncwarp();
       }
       s_in = s_in + 1 == STAGES ? 0 : s_in + 1;
