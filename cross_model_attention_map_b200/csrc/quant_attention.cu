@@ -4,7 +4,7 @@
 //
 // Bound by the cache bytes (72 + 72 a token and head of 128 in 4 bits). One CTA takes a range of tokens
 // of one (sequence, key head) and up to eight of the query heads that share it; each of its four warps
-// streams every fourth step of 64 (or 32) tokens through a ring of copies of its own and keeps scores, softmax
+// streams every fourth step of 32 tokens through a ring of copies of its own and keeps scores, softmax
 // and output in registers:
 //
 //   S^T = K^ q^T (codes; group scales in fp32), x = S / sqrt(d) in base 2, p = 2^(x - ref),
@@ -54,10 +54,9 @@ struct AttnParams {
 
 template <int D, int KB, int VB>
 struct Ring {
-  static constexpr int kRow = D * KB / 8 + D * VB / 8 + 2 * (D / 32) * 2;    // bytes a token
-  // Tiles a step: as many as leave three CTAs an SM two stages. Twelve warps an SM were as fast as
-  // sixteen with half the tiles, and need no spills.
-  static constexpr int kTiles = kRow <= 144 ? 4 : 2, kTokens = kTiles * kTok, kStages = 2;
+  // 32 tokens a step and two stages a warp fit four CTAs an SM (three where both are 8 bits of 128). With
+  // three CTAs and 64 tokens the batch of 48 took as long and one sequence of 131071 tokens 59 us, not 49.
+  static constexpr int kTiles = 2, kTokens = kTiles * kTok, kStages = 2;
   static constexpr int K = kTokens * D * KB / 8, V = kTokens * D * VB / 8, S = kTokens * (D / 32) * 2;
   static constexpr int kStage = K + S + V + S;           // keys' codes and scales, values'
   static constexpr int kWarp = kStages * kStage;
@@ -66,7 +65,7 @@ struct Ring {
 };
 
 template <int D, int KB, int VB, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads, 3) quant_attention_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kThreads, 4) quant_attention_kernel(const AttnParams p) {
   using RB = Ring<D, KB, VB>;
   constexpr int NG = D / 32, ST = RB::kStages, SB = NG * 2, TK = RB::kTokens;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -115,126 +114,122 @@ __global__ void __launch_bounds__(kThreads, 3) quant_attention_kernel(const Attn
     // a scale of 2 or more, infinite or NaN among the step's values
     const uint4 all = lds128(vs + RB::V + lane * 16 % RB::S);
     const bool large = __any_sync(0xffffffffu, (all.x | all.y | all.z | all.w) & 0x40004000u);
-#pragma unroll 1
-    for (int h = 0; h < RB::kTiles / 2; ++h) {
-      const uint32_t mask = masks[h];
-      // scores of two tiles, to be multiplied by fq: x[t][c], c = 0, 1 row gid, 2, 3 row gid + 8
-      float x[2][4];
+    const uint32_t mask = masks[0];
+    // scores of two tiles, to be multiplied by fq: x[t][c], c = 0, 1 row gid, 2, 3 row gid + 8
+    float x[2][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-        tile_scores<D, KB>(st + (2 * h + t) * (kTok * D * KB / 8), st + RB::K + (2 * h + t) * (kTok * SB), qf,
-                           x[t]);
-      uint2 sc[2][4];                                      // the values' scales of tokens tid + 4 k
+    for (int t = 0; t < 2; ++t)
+      tile_scores<D, KB>(st + t * (kTok * D * KB / 8), st + RB::K + t * (kTok * SB), qf, x[t]);
+    uint2 sc[2][4];                                      // the values' scales of tokens tid + 4 k
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        sc[t][k] = lds_scales<NG>(vs + RB::V + (16 * t + tid + 4 * k) * SB);
+    if (mask != 0xffffffffu) {
+      // tokens that do not exist: no probability, and no scale (memory behind them may hold anything)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!((mask >> (16 * t + t0)) & 1)) x[t][0] = x[t][1] = -INFINITY;
+        if (!((mask >> (16 * t + t0 + 8)) & 1)) x[t][2] = x[t][3] = -INFINITY;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          sc[t][k] = lds_scales<NG>(vs + RB::V + (32 * h + 16 * t + tid + 4 * k) * SB);
-      if (mask != 0xffffffffu) {
-        // tokens that do not exist: no probability, and no scale (memory behind them may hold anything)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!((mask >> (16 * t + t0)) & 1)) x[t][0] = x[t][1] = -INFINITY;
-          if (!((mask >> (16 * t + t0 + 8)) & 1)) x[t][2] = x[t][3] = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (!((mask >> (16 * t + tid + 4 * k)) & 1)) sc[t][k] = make_uint2(0, 0);
-        }
+          if (!((mask >> (16 * t + tid + 4 * k)) & 1)) sc[t][k] = make_uint2(0, 0);
       }
-      const float m0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-      const float m1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-      const bool slow = __any_sync(0xffffffffu, m0 > most[0] || m1 > most[1] || large);
-      if (slow) {
+    }
+    const float m0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+    const float m1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+    const bool slow = __any_sync(0xffffffffu, m0 > most[0] || m1 > most[1] || large);
+    if (slow) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float m = c ? m1 : m0;
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-          if (m > most[c]) {
-            const float r = fmaf(m, fq[c], -8.f), f = ex2(ref[c] - r);
-            ref[c] = r;
-            most[c] = (r + 14.f) / fq[c];
-            l[c] *= f;
+      for (int c = 0; c < 2; ++c) {
+        float m = c ? m1 : m0;
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        if (m > most[c]) {
+          const float r = fmaf(m, fq[c], -8.f), f = ex2(ref[c] - r);
+          ref[c] = r;
+          most[c] = (r + 14.f) / fq[c];
+          l[c] *= f;
 #pragma unroll
-            for (int k = 0; k < 2 * NG; ++k) o[k][c] *= f, o[k][c + 2] *= f;
-          }
+          for (int k = 0; k < 2 * NG; ++k) o[k][c] *= f, o[k][c + 2] *= f;
         }
+        __syncwarp();
       }
-      // probabilities as the operand of the second product: pb[t][0] tokens (tid, tid + 4), [1] + 8
-      uint32_t pb[2][2];
-      float e[2][4];
-      auto probabilities = [&]() {
+    }
+    // probabilities as the operand of the second product: pb[t][0] tokens (tid, tid + 4), [1] + 8
+    uint32_t pb[2][2];
+    float e[2][4];
+    auto probabilities = [&]() {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          pb[t][0] = movmatrix_trans(pack_f16(e[t][0], e[t][1]));
-          pb[t][1] = movmatrix_trans(pack_f16(e[t][2], e[t][3]));
-        }
-      };
+      for (int t = 0; t < 2; ++t) {
+        pb[t][0] = movmatrix_trans(pack_f16(e[t][0], e[t][1]));
+        pb[t][1] = movmatrix_trans(pack_f16(e[t][2], e[t][3]));
+      }
+    };
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) e[t][c] = ex2(fmaf(x[t][c], fq[c & 1], -ref[c & 1]));
+    probabilities();
+    if (large) {
+      __half2 top = __float2half2_rn(0.f);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) e[t][c] = ex2(fmaf(x[t][c], fq[c & 1], -ref[c & 1]));
-      probabilities();
-      if (large) {
-        __half2 top = __float2half2_rn(0.f);
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t w = hmul2(pb[t][k], scale_pair(sc[t] + 2 * k, g));
+            top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&w)));
+          }
+      if (__any_sync(0xffffffffu,
+                     __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f)))) {
+        // column gid's largest product, and the power of two that brings it under 2^14
+        float big = 0.f;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const uint32_t w = hmul2(pb[t][k], scale_pair(sc[t] + 2 * k, g));
-              top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&w)));
+              const float2 a = unpack_f16(pb[t][k]), s = unpack_f16(scale_pair(sc[t] + 2 * k, g));
+              const float u = fabsf(a.x * s.x), v = fabsf(a.y * s.y);
+              big = fmaxf(big, fmaxf(u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f));
             }
-        if (__any_sync(0xffffffffu,
-                       __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f)))) {
-          // column gid's largest product, and the power of two that brings it under 2^14
-          float big = 0.f;
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const int down = big > 32768.f ? (int)(__float_as_uint(big) >> 23) - 127 - 13 : 0;
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+        for (int c = 0; c < 2; ++c) {
+          const int n = __shfl_sync(0xffffffffu, down, 8 * tid + 4 * c);
+          const float f = __uint_as_float((uint32_t)(127 - n) << 23);
+          ref[c] += (float)n;
+          if (n != 0) most[c] = (ref[c] + 14.f) / fq[c];
+          l[c] *= f;
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
+          for (int k = 0; k < 2 * NG; ++k) o[k][c] *= f, o[k][c + 2] *= f;
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float2 a = unpack_f16(pb[t][k]), s = unpack_f16(scale_pair(sc[t] + 2 * k, g));
-                const float u = fabsf(a.x * s.x), v = fabsf(a.y * s.y);
-                big = fmaxf(big, fmaxf(u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f));
-              }
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-          const int down = big > 32768.f ? (int)(__float_as_uint(big) >> 23) - 127 - 13 : 0;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int n = __shfl_sync(0xffffffffu, down, 8 * tid + 4 * c);
-            if (n == 0) continue;
-            const float f = __uint_as_float((uint32_t)(127 - n) << 23);
-            ref[c] += (float)n;
-            most[c] = (ref[c] + 14.f) / fq[c];
-            l[c] *= f;
-#pragma unroll
-            for (int k = 0; k < 2 * NG; ++k) o[k][c] *= f, o[k][c + 2] *= f;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) e[t][c] *= f, e[t][c + 2] *= f;
-          }
-          probabilities();
+          for (int t = 0; t < 2; ++t) e[t][c] *= f, e[t][c + 2] *= f;
         }
+        probabilities();
       }
-      l[0] += (e[0][0] + e[0][2]) + (e[1][0] + e[1][2]);
-      l[1] += (e[0][1] + e[0][3]) + (e[1][1] + e[1][3]);
+    }
+    l[0] += (e[0][0] + e[0][2]) + (e[1][0] + e[1][2]);
+    l[1] += (e[0][1] + e[0][3]) + (e[1][1] + e[1][3]);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        ValueTile<D, VB> vt;
-        vt.load(vs + (2 * h + t) * (kTok * D * VB / 8));
+    for (int t = 0; t < 2; ++t) {
+      ValueTile<D, VB> vt;
+      vt.load(vs + t * (kTok * D * VB / 8));
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const uint32_t w0 = hmul2(pb[t][0], scale_pair(sc[t], g));
-          const uint32_t w1 = hmul2(pb[t][1], scale_pair(sc[t] + 2, g));
-          uint32_t r[4], q[4];
-          vt.group(g, r, q);
-          mma_f16(o[2 * g], r[0], r[1], q[0], q[1], w0, w1);
-          mma_f16(o[2 * g + 1], r[2], r[3], q[2], q[3], w0, w1);
-        }
+      for (int g = 0; g < NG; ++g) {
+        const uint32_t w0 = hmul2(pb[t][0], scale_pair(sc[t], g));
+        const uint32_t w1 = hmul2(pb[t][1], scale_pair(sc[t] + 2, g));
+        uint32_t r[4], q[4];
+        vt.group(g, r, q);
+        mma_f16(o[2 * g], r[0], r[1], q[0], q[1], w0, w1);
+        mma_f16(o[2 * g + 1], r[2], r[3], q[2], q[3], w0, w1);
       }
     }
     __syncwarp();
@@ -345,11 +340,10 @@ __global__ void __launch_bounds__(kJoinThreads) quant_attention_join_kernel(Attn
   if (p.lse && threadIdx.x == 0) p.lse[row] = z == 0.f ? -INFINITY : (m + log2f(z)) * kLn2;
 }
 
-// Ranges: enough CTAs to fill the device's 148 SMs three times over, at least 256 tokens (a step a
-// warp) and at most 2048 each, so that one long sequence in a ragged batch is still spread.
+// Ranges: enough CTAs to fill the device's 148 SMs four times over, at least 256 tokens and at most 2048 each, so that one long sequence in a ragged batch is still spread.
 void attention_split(int batch, int units, int max_ctx, int* chunk, int* splits) {
   const int64_t total = (int64_t)units * max_ctx;
-  int64_t c = (total + 148 * 3 - 1) / (148 * 3);
+  int64_t c = (total + 148 * 4 - 1) / (148 * 4);
   c = (c + 255) / 256 * 256;
   *chunk = (int)std::min<int64_t>(2048, std::max<int64_t>(256, c));
   while ((max_ctx - 1) / *chunk >= 65535) *chunk *= 2;      // the grid's third dimension

@@ -36,10 +36,11 @@ struct RowsParams {
 
 template <int D, int BITS, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 5) quant_rows_kernel(const RowsParams p) {
-  constexpr int NG = D / 32, SB = NG * 2, K = kPair * D * BITS / 8, kStage = K + kPair * SB;
-  constexpr int ST = kStage <= 2304 ? 4 : 2;
+  // 64 tokens a step where a warp's two stages of them take at most 9 KB
+  constexpr int NG = D / 32, SB = NG * 2, R = D * BITS / 8, TI = R <= 64 ? 4 : 2, TK = TI * kTok;
+  constexpr int K = TK * R, kStage = K + TK * SB, ST = 2;
   __shared__ __align__(128) uint8_t smem[kWarps * ST * kStage];
-  __shared__ StreamShared<2, ST> shared[kWarps];
+  __shared__ StreamShared<TI, ST> shared[kWarps];
   __shared__ float2 ml_s[kWarps][kHeads];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tid = lane & 3;
   let_next_start();
@@ -49,8 +50,8 @@ __global__ void __launch_bounds__(kThreads, 5) quant_rows_kernel(const RowsParam
   if (j0 >= j1) return;
   const int h0 = hk * p.group + ht * kHeads;
   const int nh = min(kHeads, p.group - ht * kHeads);
-  Stream<ALIGNED, 2, 2, ST> in;
-  in.init(&p.k, b, hk, j0 + warp * kPair, kWarps * kPair, j1, p.status,
+  Stream<ALIGNED, TI, 2, ST> in;
+  in.init(&p.k, b, hk, j0 + warp * TK, kWarps * TK, j1, p.status,
           smem_u32(smem) + warp * ST * kStage, &shared[warp]);
   in.template add<0>(p.k.codes, D * BITS / 8);
   in.template add<1>(p.k.scales, SB);
@@ -62,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, 5) quant_rows_kernel(const RowsParam
   // a reference near the maximum, moved when a score exceeds it by more than 64 (sums stay in fp32)
   float ref[2] = {kNoRef, kNoRef}, l[2] = {0.f, 0.f};
   const int t0 = (gid >> 1) + 4 * (gid & 1);
-  const int jw = j0 + warp * kPair + t0;
+  const int jw = j0 + warp * TK + t0;
   float* row0 = p.rows + ((int64_t)b * p.Hq + h0 + 2 * tid) * p.stride + jw;
 
   for (int i = 0; i < in.nsteps; ++i) {
@@ -70,48 +71,52 @@ __global__ void __launch_bounds__(kThreads, 5) quant_rows_kernel(const RowsParam
     uint32_t st;
     const uint32_t* masks;
     if (!in.take(&st, &masks)) break;
-    const uint32_t mask = masks[0];
-    float x[2][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      tile_scores<D, BITS>(st + t * (K / 2), st + K + t * (kTok * SB), qf, x[t]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) x[t][c] *= fq[c & 1];
-    }
-    if (mask != 0xffffffffu) {
+    for (int h = 0; h < TI / 2; ++h) {
+      const uint32_t mask = masks[h];
+      float x[2][4];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (!((mask >> (16 * t + t0)) & 1)) x[t][0] = x[t][1] = -INFINITY;
-        if (!((mask >> (16 * t + t0 + 8)) & 1)) x[t][2] = x[t][3] = -INFINITY;
-      }
-    }
-    const float m0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-    const float m1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-    if (__any_sync(0xffffffffu, m0 > ref[0] + 64.f || m1 > ref[1] + 64.f)) {
+        tile_scores<D, BITS>(st + (2 * h + t) * (kTok * R), st + K + (2 * h + t) * (kTok * SB), qf, x[t]);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float m = c ? m1 : m0;
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        if (m > ref[c] + 64.f) {
-          l[c] *= ex2(ref[c] - m);
-          ref[c] = m;
+        for (int c = 0; c < 4; ++c) x[t][c] *= fq[c & 1];
+      }
+      if (mask != 0xffffffffu) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!((mask >> (16 * t + t0)) & 1)) x[t][0] = x[t][1] = -INFINITY;
+          if (!((mask >> (16 * t + t0 + 8)) & 1)) x[t][2] = x[t][3] = -INFINITY;
         }
       }
-    }
-    const int at = i * kWarps * kPair;
+      const float m0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+      const float m1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+      if (__any_sync(0xffffffffu, m0 > ref[0] + 64.f || m1 > ref[1] + 64.f)) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        l[c] += ex2(x[t][c] - ref[c]) + ex2(x[t][c + 2] - ref[c]);
-        if (2 * tid + c < nh) {
-          float* dst = row0 + (int64_t)c * p.stride + at + 16 * t;
-          if (jw + at + 16 * t < j1) dst[0] = x[t][c];
-          if (jw + at + 16 * t + 8 < j1) dst[8] = x[t][c + 2];
+        for (int c = 0; c < 2; ++c) {
+          float m = c ? m1 : m0;
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          if (m > ref[c] + 64.f) {
+            l[c] *= ex2(ref[c] - m);
+            ref[c] = m;
+          }
+          __syncwarp();
         }
       }
+      const int at = i * kWarps * TK + h * kPair;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          l[c] += ex2(x[t][c] - ref[c]) + ex2(x[t][c + 2] - ref[c]);
+          if (2 * tid + c < nh) {
+            float* dst = row0 + (int64_t)c * p.stride + at + 16 * t;
+            if (jw + at + 16 * t < j1) dst[0] = x[t][c];
+            if (jw + at + 16 * t + 8 < j1) dst[8] = x[t][c + 2];
+          }
+        }
+    }
     __syncwarp();
   }
   if (!ALIGNED) cp_async_wait<0>();
@@ -163,8 +168,8 @@ __global__ void __launch_bounds__(256) quant_rows_norm_kernel(RowsParams p, int 
 void rows_split(int units, int max_ctx, int* chunk, int* splits) {
   const int64_t total = (int64_t)units * max_ctx;
   int64_t c = (total + 148 * 5 - 1) / (148 * 5);
-  c = (c + kWarps * kPair - 1) / (kWarps * kPair) * (kWarps * kPair);
-  *chunk = (int)std::min<int64_t>(2048, std::max<int64_t>(kWarps * kPair, c));
+  c = (c + 255) / 256 * 256;
+  *chunk = (int)std::min<int64_t>(2048, std::max<int64_t>(256, c));
   while ((max_ctx - 1) / *chunk >= 65535) *chunk *= 2;      // the grid's third dimension
   *splits = std::max(1, (max_ctx + *chunk - 1) / *chunk);
 }

@@ -37,8 +37,7 @@ constexpr int kTok = 16;                       // tokens a tile
 constexpr int kPair = 2 * kTok;                // tokens of one mask
 
 // Loads from shared addresses. Plain loads, not asm: the compiler may move them among the matrix
-// instructions, but not across the waits (asm volatile would keep every one of them in place; the
-// attention kernel then took 165 us where it takes @@ now, 48 sequences of up to 16384 tokens).
+// instructions, but not across the waits.
 template <typename T>
 __device__ __forceinline__ T lds(uint32_t a) {
   return *static_cast<const T*>(__cvta_shared_to_generic(a));
@@ -92,14 +91,15 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t h) {
 }
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t d;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 
-// D = A (16 x 16 fp16, row) . B (16 x 8 fp16, col) + D in fp32.
+// D = A (16 x 16 fp16, row) . B (16 x 8 fp16, col) + D in fp32. Volatile, as every instruction here that
+// takes the whole warp: the compiler may otherwise copy it into branches that only some lanes take.
 __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -107,7 +107,7 @@ __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint
 // D = A . B
 __device__ __forceinline__ void mma_f16_first(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%10,%10,%10,%10};\n"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));

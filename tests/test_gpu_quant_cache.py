@@ -13,7 +13,14 @@ bf16 one):
   mapped                     (ctx / 8 + H_s + 32) 2u sum |w| |v|: the weights' own sum, their two fp16
                              parts (2^-22), and the accumulation in steps of 16 tokens over any split
   attention                  half a bf16 step of the result, + sum p |v| times twice the scores' error
-                             and 3 u11 (the probability, the scale product and its use)
+                             and 3 u11 (the probability, the scale product and its use), + the absolute
+                             step of fp16. A probability is held as p' = 2^(x - ref) and used as p' s, each
+                             rounded to at worst 2^-25 where it is subnormal, so a token's term p' s c is
+                             off by at most 2^-25 (s + 1) Q, in units of 2^(ref - lse). ref is 8 or more
+                             below the largest score, and higher only where a p' s would pass 2^15: it is
+                             then raised until the largest lies between 2^13 and 2^14, so that
+                             2^(ref - lse) <= max(2^-8, 2^-13 s) and n tokens give
+                             n 2^-25 (s + 1) Q max(2^-8, 2^-13 s), s the largest scale
 """
 
 import math
@@ -414,6 +421,12 @@ def check_attention(got, lse, q, k, v, kb, vb, table, lens, page):
     ref, mag = Q.weighted_values(p, *v, vb, table, lens, page)
     st = score_tol(q, *k, kb, table, lens, page)[:, None, None]
     tol = 2.0 ** -8 * np.abs(ref) + (2 * st + 3 * 2.0 ** -11) * mag
+    for b, n in enumerate(lens):
+        pos = np.arange(n)
+        pg = table[b, pos // page]
+        ok = (pg >= 0) & (pg < v[1].shape[0])
+        s = v[1][pg[ok], :, pos[ok] % page].astype(np.float64).max(initial=0.0)
+        tol[b] += n * 2.0 ** -25 * (s + 1) * Q.LEVELS[vb] * max(2.0 ** -8, 2.0 ** -13 * s)
     err = np.abs(got - ref)
     assert (err <= tol).all(), (err / np.maximum(tol, 1e-300)).max()
     if lse is not None:
