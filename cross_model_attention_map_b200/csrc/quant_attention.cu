@@ -340,12 +340,14 @@ __global__ void __launch_bounds__(kJoinThreads) quant_attention_join_kernel(Attn
   if (p.lse && threadIdx.x == 0) p.lse[row] = z == 0.f ? -INFINITY : (m + log2f(z)) * kLn2;
 }
 
-// Ranges: enough CTAs to fill the device's 148 SMs four times over, at least 256 tokens and at most 2048 each, so that one long sequence in a ragged batch is still spread.
+// Ranges: enough CTAs to fill the device's 148 SMs four times over, at least 256 tokens and at most 2048
+// each, so that one long sequence in a ragged batch is still spread; one range up to 512 tokens, which
+// saves the second kernel.
 void attention_split(int batch, int units, int max_ctx, int* chunk, int* splits) {
   const int64_t total = (int64_t)units * max_ctx;
   int64_t c = (total + 148 * 4 - 1) / (148 * 4);
   c = (c + 255) / 256 * 256;
-  *chunk = (int)std::min<int64_t>(2048, std::max<int64_t>(256, c));
+  *chunk = max_ctx <= 512 ? 512 : (int)std::min<int64_t>(2048, std::max<int64_t>(256, c));
   while ((max_ctx - 1) / *chunk >= 65535) *chunk *= 2;      // the grid's third dimension
   *splits = std::max(1, (max_ctx + *chunk - 1) / *chunk);
 }

@@ -5,7 +5,7 @@
 // Bound by the key bytes (36 a token and head of 64 in 4 bits) and the rows written (4 bytes a token
 // and query head). The first kernel streams the keys as quant_attention.cu does, writes x in place of p
 // and the (reference, sum) of each range of tokens; the second joins a row's ranges in their order and
-// normalises its tokens, which are still in L2.
+// normalises its tokens, which are still in L2. Where max_ctx fits one range the first kernel does it all.
 #include <algorithm>
 
 #include "internal.h"
@@ -27,6 +27,7 @@ struct RowsParams {
   const int32_t* ctx_lens;
   int max_ctx, batch, Hq, group, htiles;
   int chunk, splits;
+  bool single;                       // the first kernel normalises its rows: one range, a short stride
   float scale_log2;
   float* rows;                       // [batch, Hq, stride]
   int stride;
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(kThreads, 5) quant_rows_kernel(const RowsParam
   const int hk = blockIdx.x / p.htiles, ht = blockIdx.x - hk * p.htiles, b = blockIdx.y, split = blockIdx.z;
   const int ctx = quant_ctx(p.ctx_lens, b, p.max_ctx, p.status);
   const int j0 = split * p.chunk, j1 = min(ctx, j0 + p.chunk);
-  if (j0 >= j1) return;
+  if (j0 >= j1 && !p.single) return;
   const int h0 = hk * p.group + ht * kHeads;
   const int nh = min(kHeads, p.group - ht * kHeads);
   Stream<ALIGNED, TI, 2, ST> in;
@@ -134,7 +135,18 @@ __global__ void __launch_bounds__(kThreads, 5) quant_rows_kernel(const RowsParam
     for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml_s[w][threadIdx.x].x);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) z += ml_s[w][threadIdx.x].y * ex2(ml_s[w][threadIdx.x].x - m);
-    p.ml[((int64_t)b * p.Hq + h0 + threadIdx.x) * p.splits + split] = make_float2(m, z);
+    if (!p.single)
+      p.ml[((int64_t)b * p.Hq + h0 + threadIdx.x) * p.splits + split] = make_float2(m, z);
+    else
+      ml_s[0][threadIdx.x].x = z == 0.f ? INFINITY : m + log2f(z);
+  }
+  if (!p.single) return;
+  __syncthreads();                                           // this CTA wrote all of its rows' scores
+  for (int h = warp; h < nh; h += kWarps) {
+    float* row = p.rows + ((int64_t)b * p.Hq + h0 + h) * p.stride;
+    const float lse = ml_s[0][h].x;
+    for (int j = lane; j < p.stride; j += 32)
+      row[j] = j < ctx && lse != INFINITY ? ex2(row[j] - lse) : 0.f;
   }
 }
 
@@ -169,7 +181,7 @@ void rows_split(int units, int max_ctx, int* chunk, int* splits) {
   const int64_t total = (int64_t)units * max_ctx;
   int64_t c = (total + 148 * 5 - 1) / (148 * 5);
   c = (c + 255) / 256 * 256;
-  *chunk = (int)std::min<int64_t>(2048, std::max<int64_t>(256, c));
+  *chunk = max_ctx <= 512 ? 512 : (int)std::min<int64_t>(2048, std::max<int64_t>(256, c));
   while ((max_ctx - 1) / *chunk >= 65535) *chunk *= 2;      // the grid's third dimension
   *splits = std::max(1, (max_ctx + *chunk - 1) / *chunk);
 }
@@ -186,6 +198,7 @@ int launch_d(const RowsParams& p, int bits, cudaStream_t st) {
     else quant_rows_kernel<D, 8, false><<<grid, kThreads, 0, st>>>(p);
   }
   IAMAP_LAUNCH_CHECK("quant_rows_kernel");
+  if (p.single) return IAMAP_OK;
   const int parts = (p.stride + kNormTokens - 1) / kNormTokens;
   return launch_next("quant_rows_norm_kernel", quant_rows_norm_kernel,
                      dim3((unsigned int)((int64_t)p.batch * p.Hq * parts)), 256, 0, st, p, parts);
@@ -235,6 +248,7 @@ extern "C" int iamap_sender_rows_quant(const void* q, const void* k_codes, const
       (int64_t)batch * H_s * ((ctx_stride + (int64_t)kNormTokens - 1) / kNormTokens) > 0x7fffffff)
     return set_error(IAMAP_ERR_UNSUPPORTED, "batch above 65535, or batch times heads times ctx_stride too large");
   rows_split((int)units, max_ctx, &p.chunk, &p.splits);
+  p.single = p.splits == 1 && ctx_stride <= kNormTokens;
   const size_t need = sizeof(float2) * (size_t)batch * H_s * p.splits;
   if (!ws || ws_bytes < need)
     return set_error(IAMAP_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws_bytes);

@@ -229,6 +229,7 @@ class QuantCache:
         return num_seqs, self._table(page_table, num_seqs)
 
     def _table(self, page_table, num_seqs):
+        """Checks a page table; its pages per sequence."""
         if self.device.index != torch._C._cuda_getDevice():
             raise ValueError("the cache lies on %s, which is not the current device" % self.device)
         shape = page_table.shape
