@@ -62,12 +62,24 @@ struct MappedParams {
 __device__ __forceinline__ float pow2i(int k) {
   return __uint_as_float((uint32_t)(min(max(k, -126), 127) + 127) << 23);
 }
-// The weights: a CTA a range of tokens for eight receivers, two tokens a thread.
+// (a, b) += (c, c) (x, y)
+__device__ __forceinline__ void fma2(float2& a, float2 x, float c) {
+  uint64_t d = *reinterpret_cast<uint64_t*>(&a);
+  const float2 cc = make_float2(c, c);
+  asm("fma.rn.f32x2 %0, %1, %2, %0;"
+      : "+l"(d) : "l"(*reinterpret_cast<const uint64_t*>(&x)), "l"(*reinterpret_cast<const uint64_t*>(&cc)));
+  a = *reinterpret_cast<float2*>(&d);
+}
+// Weights of 32 tokens and one unit: of the tokens t and t + 4 the pair of high parts and the pair of low
+// parts, [4 groups of 8 tokens][RJ / 4][t = 0..3][receiver] for four and eight receivers, [4][t] for one:
+// the order in which a warp's lanes want them.
+//
+// The weights: a CTA a range of tokens for eight receivers; a thread has the tokens j and j + 4.
 constexpr int kWeightThreads = kChunk / 2;
 template <int RJ>
 __global__ void __launch_bounds__(kWeightThreads) quant_weights_kernel(const MappedParams p) {
   constexpr int UN = 8 / RJ;                                 // units a CTA
-  extern __shared__ float W_s[];                             // [H_s][8]
+  extern __shared__ __align__(16) float W_s[];               // [H_s][8]
   __shared__ uint32_t max_s[8];
   let_next_start();
   const int lane = threadIdx.x & 31, b = blockIdx.y, chunk = blockIdx.z, u0 = blockIdx.x * UN;
@@ -81,48 +93,78 @@ __global__ void __launch_bounds__(kWeightThreads) quant_weights_kernel(const Map
   }
   if (threadIdx.x < 8) max_s[threadIdx.x] = 0;
   __syncthreads();
-  const int j = chunk * kChunk + threadIdx.x;
-  const bool there[2] = {j < ctx, j + kWeightThreads < ctx};
-  const float* row = p.rows + (int64_t)b * p.H_s * p.stride + j;
-  float w[2][8];
+  const int j = chunk * kChunk + (threadIdx.x >> 2) * 8 + (threadIdx.x & 3);
+  // tokens that do not exist read the last one's row and get the weight 0
+  const bool there[2] = {j < ctx, j + 4 < ctx};
+  const float* row = p.rows + (int64_t)b * p.H_s * p.stride + min(j, ctx - 1);
+  const int next = there[1] ? 4 : 0;
+  float2 w[2][4];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) w[0][k] = w[1][k] = 0.f;
-#pragma unroll 8
-  for (int s = 0; s < p.H_s; ++s, row += p.stride) {
-    const float x = there[0] ? __ldg(row) : 0.f, y = there[1] ? __ldg(row + kWeightThreads) : 0.f;
+  for (int k = 0; k < 4; ++k) w[0][k] = w[1][k] = make_float2(0.f, 0.f);
+  auto add = [&](int s, float x, float y) {
     const float4 f0 = *reinterpret_cast<const float4*>(W_s + s * 8);
     const float4 f1 = *reinterpret_cast<const float4*>(W_s + s * 8 + 4);
-    const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+    const float2 f[4] = {{f0.x, f0.y}, {f0.z, f0.w}, {f1.x, f1.y}, {f1.z, f1.w}};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w[0][k] = fmaf(f[k], x, w[0][k]), w[1][k] = fmaf(f[k], y, w[1][k]);
+    for (int k = 0; k < 4; ++k) fma2(w[0][k], f[k], x), fma2(w[1][k], f[k], y);
+  };
+  int s = 0;
+  for (; s + 8 <= p.H_s; s += 8, row += 8 * (int64_t)p.stride) {
+    float x[8], y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __ldg(row + (int64_t)e * p.stride), y[e] = __ldg(row + (int64_t)e * p.stride + next);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) add(s + e, x[e], y[e]);
   }
+  if (s < p.H_s) {
+    float x[8], y[8];
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (s + e < p.H_s) x[e] = __ldg(row + (int64_t)e * p.stride), y[e] = __ldg(row + (int64_t)e * p.stride + next);
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (s + e < p.H_s) add(s + e, x[e], y[e]);
+  }
+  float v[2][8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     // a weight of a token that does not exist is 0, whatever W holds
-    w[0][k] = there[0] ? w[0][k] : 0.f;
-    w[1][k] = there[1] ? w[1][k] : 0.f;
-    const uint32_t m = __reduce_max_sync(0xffffffffu, max(__float_as_uint(w[0][k]) & 0x7fffffffu,
-                                                          __float_as_uint(w[1][k]) & 0x7fffffffu));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) v[h][k] = there[h] ? (k & 1 ? w[h][k / 2].y : w[h][k / 2].x) : 0.f;
+    const uint32_t m = __reduce_max_sync(0xffffffffu, max(__float_as_uint(v[0][k]) & 0x7fffffffu,
+                                                          __float_as_uint(v[1][k]) & 0x7fffffffu));
     if (lane == k) atomicMax(&max_s[k], m);
   }
   __syncthreads();
-  const int n = p.chunks * (kChunk / kBlock), block = chunk * (kChunk / kBlock) + (threadIdx.x >> 5);
+  const int n = p.chunks * (kChunk / kBlock), block = chunk * (kChunk / kBlock) + (threadIdx.x >> 4);
   uint32_t* rec = reinterpret_cast<uint32_t*>(p.records) + (((int64_t)b * p.units + u0) * n + block) * (RJ * kBlock);
+  uint2 parts[8];                                            // (high, low)
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    if (u0 + k / RJ >= p.units) break;
     // infinities and NaN stay what they are
     const uint32_t m = max_s[k];
     const int up = m == 0 || m >= 0x7f800000u ? 0 : min(13 - ((int)(m >> 23) - 127), 126);
-    const float f = pow2i(up);
-    uint32_t* to = rec + (int64_t)(k / RJ) * n * (RJ * kBlock) + k % RJ * kBlock + lane;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float x = w[h][k] * f, high = __half2float(__float2half_rn(x));
-      to[h * (kWeightThreads / kBlock) * (RJ * kBlock)] = pack_f16(high, x - high);
-    }
-    if (threadIdx.x == k)
+    const float f = pow2i(up), x = v[0][k] * f, y = v[1][k] * f;
+    const uint32_t high = pack_f16(x, y);
+    const float2 back = unpack_f16(high);
+    parts[k] = make_uint2(high, pack_f16(x - back.x, y - back.y));
+    if (threadIdx.x == k && u0 + k / RJ < p.units)
       p.powers[(((int64_t)b * p.units + u0 + k / RJ) * p.chunks + chunk) * RJ + k % RJ] = up;
+  }
+  const int eight = (threadIdx.x >> 2) & 3, t = threadIdx.x & 3;
+  if (RJ == 1) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (u0 + k < p.units) *reinterpret_cast<uint2*>(rec + (int64_t)k * n * kBlock + eight * 8 + t * 2) = parts[k];
+  } else {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if (RJ == 4 && u0 + c >= p.units) break;
+      uint32_t* to = rec + (RJ == 4 ? (int64_t)c * n * (4 * kBlock) + eight * 32 : (eight * 2 + c) * 32) + t * 8;
+      const uint2* from = parts + 4 * c;
+      *reinterpret_cast<uint4*>(to) = make_uint4(from[0].x, from[0].y, from[1].x, from[1].y);
+      *reinterpret_cast<uint4*>(to + 4) = make_uint4(from[2].x, from[2].y, from[3].x, from[3].y);
+    }
   }
 }
 
@@ -181,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
   // The operand of a column is rn(l' s + (h' s - rn(h' s))): a low column has h' = h, l' = l, a high one
   // h' = 0, l' = h.
   const bool lo = gid & 1;
-  const uint32_t own = lo ? 0x3c003c00u : 0u, take_l = lo ? 0x7632u : 0x5410u;
+  const uint32_t own = lo ? 0xffffffffu : 0u;
   int E = 0;                                                 // the scales are taken times 2^-E
   uint32_t down = 0x3c003c00u;                               // 2^-E
 
@@ -191,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
     const uint32_t* masks;
     if (!in.take(&st, &masks)) break;
     const uint32_t scales = st + TK * R;
-    const uint32_t weights = scales + TK * SB + (GM == 0 ? 0 : gid >> 1) * (kBlock * 4) + tid * 4;
+    const uint32_t weights = scales + TK * SB + (GM == 0 ? tid * 8 : tid * 32 + (gid >> 1) * 8);
     // a scale of 2 or more (infinite, NaN) in the step
     const uint2 all = lds64(scales + lane * 8 % (TK * SB));
     const uint2 all2 = TK * SB > 256 ? lds64(scales + 256 + lane * 8) : make_uint2(0, 0);
@@ -244,10 +286,8 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
         for (int c = 0; c < CT; ++c)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint32_t at = weights + h * REC + c * (4 * kBlock * 4) + q * kTok * 4 + 32 * k;
-            const uint32_t a = lds32(at), d = lds32(at + 16);
-            hp[c][k] = hmul2(__byte_perm(a, d, 0x5410), own);
-            lp[c][k] = __byte_perm(a, d, take_l);
+            const uint2 w = lds64(weights + h * REC + (GM == 0 ? (2 * q + k) * 32 : ((2 * q + k) * CT + c) * 128));
+            hp[c][k] = w.x & own, lp[c][k] = lo ? w.y : w.x;
           }
         if (E != 0) {
           if (GM == 0) {
