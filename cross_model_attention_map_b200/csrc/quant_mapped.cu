@@ -62,108 +62,156 @@ struct MappedParams {
 __device__ __forceinline__ float pow2i(int k) {
   return __uint_as_float((uint32_t)(min(max(k, -126), 127) + 127) << 23);
 }
-// (a, b) += (c, c) (x, y)
-__device__ __forceinline__ void fma2(float2& a, float2 x, float c) {
-  uint64_t d = *reinterpret_cast<uint64_t*>(&a);
-  const float2 cc = make_float2(c, c);
-  asm("fma.rn.f32x2 %0, %1, %2, %0;"
-      : "+l"(d) : "l"(*reinterpret_cast<const uint64_t*>(&x)), "l"(*reinterpret_cast<const uint64_t*>(&cc)));
-  a = *reinterpret_cast<float2*>(&d);
+// x = b[0] + b[1] + b[2] in bf16, each part the rounding of what the ones before it leave, for a pair of values
+__device__ __forceinline__ void split3(float x, float y, uint32_t (&b)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b[i]) : "f"(y), "f"(x));
+    x -= __uint_as_float(b[i] << 16);
+    y -= __uint_as_float(b[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+               "{%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // Weights of 32 tokens and one unit: of the tokens t and t + 4 the pair of high parts and the pair of low
 // parts, [4 groups of 8 tokens][RJ / 4][t = 0..3][receiver] for four and eight receivers, [4][t] for one:
 // the order in which a warp's lanes want them.
 //
-// The weights: a CTA a range of tokens for eight receivers; a thread has the tokens j and j + 4.
-constexpr int kWeightThreads = kChunk / 2;
+// The weights: a CTA a range of tokens for sixteen receivers, a warp 64 of the tokens. The products run on
+// matrix instructions with both factors in three bf16 parts; the six products of the larger parts leave an
+// error of 2^-25 relative, below fp32's rounding. (fp32 arithmetic, eight receivers a CTA: 28 us where this
+// takes @@, 118 thousand tokens, 14 rows to 64 heads.)
+constexpr int kWeightSlots = 16, kWeightTokens = 64, kWeightThreads = kChunk / kWeightTokens * 32;
 template <int RJ>
-__global__ void __launch_bounds__(kWeightThreads) quant_weights_kernel(const MappedParams p) {
-  constexpr int UN = 8 / RJ;                                 // units a CTA
-  extern __shared__ __align__(16) float W_s[];               // [H_s][8]
-  __shared__ uint32_t max_s[8];
+__global__ void __launch_bounds__(kWeightThreads, 2) quant_weights_kernel(const MappedParams p) {
+  constexpr int UN = kWeightSlots / RJ, NT = kWeightSlots / 8, MT = kWeightTokens / 16;
+  __shared__ uint32_t max_s[kWeightSlots];
   let_next_start();
-  const int lane = threadIdx.x & 31, b = blockIdx.y, chunk = blockIdx.z, u0 = blockIdx.x * UN;
+  const int b = blockIdx.y, chunk = blockIdx.z, u0 = blockIdx.x * UN;
   const int ctx = quant_ctx(p.ctx_lens, b, p.max_ctx, p.status);
   if (chunk * kChunk >= ctx) return;
-  {
-    const int k = threadIdx.x & 7, un = u0 + k / RJ, of = un % p.rtiles * p.rj + k % RJ;
-    const bool ok = un < p.units && k % RJ < p.rj && of < p.group;
-    const float* src = p.W + ((int64_t)(un / p.rtiles) * p.group + of) * p.H_s;
-    for (int s = threadIdx.x >> 3; s < p.H_s; s += kWeightThreads / 8) W_s[s * 8 + k] = ok ? __ldg(src + s) : 0.f;
-  }
-  if (threadIdx.x < 8) max_s[threadIdx.x] = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tid = lane & 3;
+  if (threadIdx.x < kWeightSlots) max_s[threadIdx.x] = 0;
   __syncthreads();
-  const int j = chunk * kChunk + (threadIdx.x >> 2) * 8 + (threadIdx.x & 3);
-  // tokens that do not exist read the last one's row and get the weight 0
-  const bool there[2] = {j < ctx, j + 4 < ctx};
-  const float* row = p.rows + (int64_t)b * p.H_s * p.stride + min(j, ctx - 1);
-  const int next = there[1] ? 4 : 0;
-  float2 w[2][4];
+  // rows gid and gid + 8 of a matrix tile are the tokens j and j + 4
+  const int j0 = chunk * kChunk + warp * kWeightTokens, j = j0 + (gid & 3) + 8 * (gid >> 2);
+  const bool live = j0 < ctx;
+  float w[MT][NT][4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) w[0][k] = w[1][k] = make_float2(0.f, 0.f);
-  auto add = [&](int s, float x, float y) {
-    const float4 f0 = *reinterpret_cast<const float4*>(W_s + s * 8);
-    const float4 f1 = *reinterpret_cast<const float4*>(W_s + s * 8 + 4);
-    const float2 f[4] = {{f0.x, f0.y}, {f0.z, f0.w}, {f1.x, f1.y}, {f1.z, f1.w}};
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) fma2(w[0][k], f[k], x), fma2(w[1][k], f[k], y);
-  };
-  int s = 0;
-  for (; s + 8 <= p.H_s; s += 8, row += 8 * (int64_t)p.stride) {
-    float x[8], y[8];
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __ldg(row + (int64_t)e * p.stride), y[e] = __ldg(row + (int64_t)e * p.stride + next);
+      for (int e = 0; e < 4; ++e) w[m][i][e] = 0.f;
+  if (live) {
+    const float* W[NT];                                      // column gid's row of W
 #pragma unroll
-    for (int e = 0; e < 8; ++e) add(s + e, x[e], y[e]);
-  }
-  if (s < p.H_s) {
-    float x[8], y[8];
+    for (int i = 0; i < NT; ++i) {
+      const int k = 8 * i + gid, un = u0 + k / RJ, of = un % p.rtiles * p.rj + k % RJ;
+      const bool ok = un < p.units && k % RJ < p.rj && of < p.group;
+      W[i] = ok ? p.W + ((int64_t)(un / p.rtiles) * p.group + of) * p.H_s : nullptr;
+    }
+    int at[2 * MT];                                          // tokens that do not exist read the last one's row
 #pragma unroll
-    for (int e = 0; e < 7; ++e)
-      if (s + e < p.H_s) x[e] = __ldg(row + (int64_t)e * p.stride), y[e] = __ldg(row + (int64_t)e * p.stride + next);
+    for (int m = 0; m < 2 * MT; ++m) at[m] = min(j + 16 * (m >> 1) + 4 * (m & 1), ctx - 1);
+    for (int s0 = 0; s0 < p.H_s; s0 += 16) {
+      const float* row[4];
+      bool ok[4];
+      uint32_t wb[NT][2][3];
 #pragma unroll
-    for (int e = 0; e < 7; ++e)
-      if (s + e < p.H_s) add(s + e, x[e], y[e]);
-  }
-  float v[2][8];
+      for (int e = 0; e < 4; ++e) {
+        const int s = s0 + 2 * tid + (e & 1) + 8 * (e >> 1);
+        ok[e] = s < p.H_s;
+        row[e] = p.rows + ((int64_t)b * p.H_s + s) * p.stride;
+      }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    // a weight of a token that does not exist is 0, whatever W holds
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) v[h][k] = there[h] ? (k & 1 ? w[h][k / 2].y : w[h][k / 2].x) : 0.f;
-    const uint32_t m = __reduce_max_sync(0xffffffffu, max(__float_as_uint(v[0][k]) & 0x7fffffffu,
-                                                          __float_as_uint(v[1][k]) & 0x7fffffffu));
-    if (lane == k) atomicMax(&max_s[k], m);
+        for (int e = 0; e < 2; ++e) {
+          const float* f = W[i] + s0 + 2 * tid + 8 * e;
+          split3(W[i] && ok[2 * e] ? __ldg(f) : 0.f, W[i] && ok[2 * e + 1] ? __ldg(f + 1) : 0.f, wb[i][e]);
+        }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        uint32_t a[4][3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int h = 2 * (e >> 1), t = at[2 * m + (e & 1)];
+          split3(ok[h] ? __ldg(row[h] + t) : 0.f, ok[h + 1] ? __ldg(row[h + 1] + t) : 0.f, a[e]);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          constexpr int part[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
+#pragma unroll
+          for (int e = 0; e < 6; ++e) {
+            const int x = part[e][0], y = part[e][1];
+            mma_bf16(w[m][i], a[0][x], a[1][x], a[2][x], a[3][x], wb[i][0][y], wb[i][1][y]);
+          }
+        }
+      }
+    }
+    if (j0 + kWeightTokens > ctx) {
+      // a weight of a token that does not exist is 0, whatever W holds
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + 16 * m + 4 * (e >> 1) >= ctx) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) w[m][i][e] = 0.f;
+          }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {                          // column 2 tid + e
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < MT; ++k)
+          m = max(m, max(__float_as_uint(w[k][i][e]) & 0x7fffffffu, __float_as_uint(w[k][i][e + 2]) & 0x7fffffffu));
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, x));
+        if (gid == 0) atomicMax(&max_s[8 * i + 2 * tid + e], m);
+      }
   }
   __syncthreads();
-  const int n = p.chunks * (kChunk / kBlock), block = chunk * (kChunk / kBlock) + (threadIdx.x >> 4);
-  uint32_t* rec = reinterpret_cast<uint32_t*>(p.records) + (((int64_t)b * p.units + u0) * n + block) * (RJ * kBlock);
-  uint2 parts[8];                                            // (high, low)
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    // infinities and NaN stay what they are
+  if (!live) return;
+  // infinities and NaN stay what they are
+  auto power = [&](int k) {
     const uint32_t m = max_s[k];
-    const int up = m == 0 || m >= 0x7f800000u ? 0 : min(13 - ((int)(m >> 23) - 127), 126);
-    const float f = pow2i(up), x = v[0][k] * f, y = v[1][k] * f;
-    const uint32_t high = pack_f16(x, y);
-    const float2 back = unpack_f16(high);
-    parts[k] = make_uint2(high, pack_f16(x - back.x, y - back.y));
-    if (threadIdx.x == k && u0 + k / RJ < p.units)
-      p.powers[(((int64_t)b * p.units + u0 + k / RJ) * p.chunks + chunk) * RJ + k % RJ] = up;
-  }
-  const int eight = (threadIdx.x >> 2) & 3, t = threadIdx.x & 3;
-  if (RJ == 1) {
+    return m == 0 || m >= 0x7f800000u ? 0 : min(13 - ((int)(m >> 23) - 127), 126);
+  };
+  if (threadIdx.x < kWeightSlots && u0 + threadIdx.x / RJ < p.units)
+    p.powers[(((int64_t)b * p.units + u0 + threadIdx.x / RJ) * p.chunks + chunk) * RJ + threadIdx.x % RJ] =
+        power(threadIdx.x);
+  const int n = p.chunks * (kChunk / kBlock), block = j0 / kBlock;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (u0 + k < p.units) *reinterpret_cast<uint2*>(rec + (int64_t)k * n * kBlock + eight * 8 + t * 2) = parts[k];
-  } else {
+  for (int i = 0; i < NT; ++i) {
+    const float f0 = pow2i(power(8 * i + 2 * tid)), f1 = pow2i(power(8 * i + 2 * tid + 1));
+    const int un = u0 + (8 * i + 2 * tid) / RJ;
+    if (un >= p.units) continue;
+    uint32_t* rec = reinterpret_cast<uint32_t*>(p.records) + (((int64_t)b * p.units + un) * n + block) * (RJ * kBlock) +
+                    (RJ == 8 ? (tid >> 1) * 32 : 0) + (gid & 3) * (RJ == 1 ? 2 : 8) + (RJ == 1 ? 0 : (tid & 1) * 4);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      if (RJ == 4 && u0 + c >= p.units) break;
-      uint32_t* to = rec + (RJ == 4 ? (int64_t)c * n * (4 * kBlock) + eight * 32 : (eight * 2 + c) * 32) + t * 8;
-      const uint2* from = parts + 4 * c;
-      *reinterpret_cast<uint4*>(to) = make_uint4(from[0].x, from[0].y, from[1].x, from[1].y);
-      *reinterpret_cast<uint4*>(to + 4) = make_uint4(from[2].x, from[2].y, from[3].x, from[3].y);
+    for (int m = 0; m < MT; ++m) {
+      const float* c = w[m][i];
+      const float x0 = c[0] * f0, y0 = c[2] * f0, x1 = c[1] * f1, y1 = c[3] * f1;
+      uint4 v;                                               // (high, low) of two receivers
+      v.x = pack_f16(x0, y0), v.z = pack_f16(x1, y1);
+      const float2 b0 = unpack_f16(v.x), b1 = unpack_f16(v.z);
+      v.y = pack_f16(x0 - b0.x, y0 - b0.y), v.w = pack_f16(x1 - b1.x, y1 - b1.y);
+      uint32_t* to = rec + (m >> 1) * (RJ * kBlock) + ((m & 1) * 2 + (gid >> 2)) * (RJ * 8);
+      if (RJ == 1) {
+        *reinterpret_cast<uint2*>(to) = make_uint2(v.x, v.y);
+        if (un + 1 < p.units) *reinterpret_cast<uint2*>(to + (int64_t)n * kBlock) = make_uint2(v.z, v.w);
+      } else {
+        *reinterpret_cast<uint4*>(to) = v;
+      }
     }
   }
 }
@@ -435,8 +483,8 @@ size_t mapped_shape(int batch, int H_kv, int group, int d, int max_ctx, MappedPa
 
 template <int RJ>
 int launch_weights(const MappedParams& p, cudaStream_t st) {
-  const dim3 grid((p.units + 8 / RJ - 1) / (8 / RJ), p.batch, p.chunks);
-  quant_weights_kernel<RJ><<<grid, kWeightThreads, p.H_s * 8 * sizeof(float), st>>>(p);
+  constexpr int UN = kWeightSlots / RJ;
+  quant_weights_kernel<RJ><<<dim3((p.units + UN - 1) / UN, p.batch, p.chunks), kWeightThreads, 0, st>>>(p);
   IAMAP_LAUNCH_CHECK("quant_weights_kernel");
   return IAMAP_OK;
 }
