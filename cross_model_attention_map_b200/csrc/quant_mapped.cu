@@ -88,129 +88,150 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 // takes @@, 118 thousand tokens, 14 rows to 64 heads.)
 constexpr int kWeightSlots = 16, kWeightTokens = 64, kWeightThreads = kChunk / kWeightTokens * 32;
 template <int RJ>
-__global__ void __launch_bounds__(kWeightThreads, 2) quant_weights_kernel(const MappedParams p) {
+__global__ void __launch_bounds__(kWeightThreads, 2) quant_weights_kernel(const MappedParams p, int slices) {
   constexpr int UN = kWeightSlots / RJ, NT = kWeightSlots / 8, MT = kWeightTokens / 16;
-  __shared__ uint32_t max_s[kWeightSlots];
+  __shared__ uint32_t max_s[3][kWeightSlots];                // of this item, the next, and the last
   let_next_start();
-  const int b = blockIdx.y, chunk = blockIdx.z, u0 = blockIdx.x * UN;
-  const int ctx = quant_ctx(p.ctx_lens, b, p.max_ctx, p.status);
-  if (chunk * kChunk >= ctx) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tid = lane & 3;
-  if (threadIdx.x < kWeightSlots) max_s[threadIdx.x] = 0;
+  if (threadIdx.x < 3 * kWeightSlots) max_s[0][threadIdx.x] = 0;
   __syncthreads();
-  // rows gid and gid + 8 of a matrix tile are the tokens j and j + 4
-  const int j0 = chunk * kChunk + warp * kWeightTokens, j = j0 + (gid & 3) + 8 * (gid >> 2);
-  const bool live = j0 < ctx;
-  float w[MT][NT][4];
+  // Items are counted over the ranges that the sequences have, so that short ones beside a long one leave
+  // no CTAs that only find nothing to do: `ranges` of the 32 sequences from b0 on, `before` up to there.
+  int b0 = 0, before = 0, len = 0, ranges = 0, upto = 0;
+  auto lengths = [&] {
+    len = b0 + lane < p.batch ? quant_ctx(p.ctx_lens, b0 + lane, p.max_ctx, p.status) : 0;
+    upto = (len + kChunk - 1) / kChunk;
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[m][i][e] = 0.f;
-  if (live) {
-    const float* W[NT];                                      // column gid's row of W
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int k = 8 * i + gid, un = u0 + k / RJ, of = un % p.rtiles * p.rj + k % RJ;
-      const bool ok = un < p.units && k % RJ < p.rj && of < p.group;
-      W[i] = ok ? p.W + ((int64_t)(un / p.rtiles) * p.group + of) * p.H_s : nullptr;
+    for (int x = 1; x < 32; x *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, x);
+      if (lane >= x) upto += y;
     }
-    int at[2 * MT];                                          // tokens that do not exist read the last one's row
+    ranges = __shfl_sync(0xffffffffu, upto, 31);
+  };
+  lengths();
+  int now = 0;
+  for (int item = blockIdx.x;; item += gridDim.x, now = now == 2 ? 0 : now + 1) {
+    const int u0 = item % slices * UN, range = item / slices;
+    while (range - before >= ranges && b0 + 32 < p.batch) before += ranges, b0 += 32, lengths();
+    if (range - before >= ranges) return;
+    const int which = __ffs(__ballot_sync(0xffffffffu, range - before < upto)) - 1, b = b0 + which;
+    const int ctx = __shfl_sync(0xffffffffu, len, which);
+    const int chunk = range - before - (__shfl_sync(0xffffffffu, upto, which) - (ctx + kChunk - 1) / kChunk);
+    // rows gid and gid + 8 of a matrix tile are the tokens j and j + 4
+    const int j0 = chunk * kChunk + warp * kWeightTokens, j = j0 + (gid & 3) + 8 * (gid >> 2);
+    const bool live = j0 < ctx;
+    float w[MT][NT][4];
 #pragma unroll
-    for (int m = 0; m < 2 * MT; ++m) at[m] = min(j + 16 * (m >> 1) + 4 * (m & 1), ctx - 1);
-    for (int s0 = 0; s0 < p.H_s; s0 += 16) {
-      const float* row[4];
-      bool ok[4];
-      uint32_t wb[NT][2][3];
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int s = s0 + 2 * tid + (e & 1) + 8 * (e >> 1);
-        ok[e] = s < p.H_s;
-        row[e] = p.rows + ((int64_t)b * p.H_s + s) * p.stride;
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[m][i][e] = 0.f;
+    if (live) {
+      const float* W[NT];                                      // column gid's row of W
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const int k = 8 * i + gid, un = u0 + k / RJ, of = un % p.rtiles * p.rj + k % RJ;
+        const bool ok = un < p.units && k % RJ < p.rj && of < p.group;
+        W[i] = ok ? p.W + ((int64_t)(un / p.rtiles) * p.group + of) * p.H_s : nullptr;
+      }
+      int at[2 * MT];                                          // tokens that do not exist read the last one's row
+#pragma unroll
+      for (int m = 0; m < 2 * MT; ++m) at[m] = min(j + 16 * (m >> 1) + 4 * (m & 1), ctx - 1);
+      for (int s0 = 0; s0 < p.H_s; s0 += 16) {
+        const float* row[4];
+        bool ok[4];
+        uint32_t wb[NT][2][3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int s = s0 + 2 * tid + (e & 1) + 8 * (e >> 1);
+          ok[e] = s < p.H_s;
+          row[e] = p.rows + ((int64_t)b * p.H_s + s) * p.stride;
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float* f = W[i] + s0 + 2 * tid + 8 * e;
+            split3(W[i] && ok[2 * e] ? __ldg(f) : 0.f, W[i] && ok[2 * e + 1] ? __ldg(f + 1) : 0.f, wb[i][e]);
+          }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          uint32_t a[4][3];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int h = 2 * (e >> 1), t = at[2 * m + (e & 1)];
+            split3(ok[h] ? __ldg(row[h] + t) : 0.f, ok[h + 1] ? __ldg(row[h + 1] + t) : 0.f, a[e]);
+          }
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            constexpr int part[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
+#pragma unroll
+            for (int e = 0; e < 6; ++e) {
+              const int x = part[e][0], y = part[e][1];
+              mma_bf16(w[m][i], a[0][x], a[1][x], a[2][x], a[3][x], wb[i][0][y], wb[i][1][y]);
+            }
+          }
+        }
+      }
+      if (j0 + kWeightTokens > ctx) {
+        // a weight of a token that does not exist is 0, whatever W holds
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j + 16 * m + 4 * (e >> 1) >= ctx) {
+#pragma unroll
+              for (int i = 0; i < NT; ++i) w[m][i][e] = 0.f;
+            }
       }
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float* f = W[i] + s0 + 2 * tid + 8 * e;
-          split3(W[i] && ok[2 * e] ? __ldg(f) : 0.f, W[i] && ok[2 * e + 1] ? __ldg(f + 1) : 0.f, wb[i][e]);
+        for (int e = 0; e < 2; ++e) {                          // column 2 tid + e
+          uint32_t m = 0;
+#pragma unroll
+          for (int k = 0; k < MT; ++k)
+            m = max(m, max(__float_as_uint(w[k][i][e]) & 0x7fffffffu, __float_as_uint(w[k][i][e + 2]) & 0x7fffffffu));
+#pragma unroll
+          for (int x = 4; x < 32; x *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, x));
+          if (gid == 0) atomicMax(&max_s[now][8 * i + 2 * tid + e], m);
         }
+    }
+    if (threadIdx.x < kWeightSlots) max_s[now == 2 ? 0 : now + 1][threadIdx.x] = 0;
+    __syncthreads();
+    if (!live) continue;
+    // infinities and NaN stay what they are
+    auto power = [&](int k) {
+      const uint32_t m = max_s[now][k];
+      return m == 0 || m >= 0x7f800000u ? 0 : min(13 - ((int)(m >> 23) - 127), 126);
+    };
+    if (threadIdx.x < kWeightSlots && u0 + threadIdx.x / RJ < p.units)
+      p.powers[(((int64_t)b * p.units + u0 + threadIdx.x / RJ) * p.chunks + chunk) * RJ + threadIdx.x % RJ] =
+          power(threadIdx.x);
+    const int n = p.chunks * (kChunk / kBlock), block = j0 / kBlock;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const float f0 = pow2i(power(8 * i + 2 * tid)), f1 = pow2i(power(8 * i + 2 * tid + 1));
+      const int un = u0 + (8 * i + 2 * tid) / RJ;
+      if (un >= p.units) continue;
+      uint32_t* rec = reinterpret_cast<uint32_t*>(p.records) + (((int64_t)b * p.units + un) * n + block) * (RJ * kBlock) +
+                      (RJ == 8 ? (tid >> 1) * 32 : 0) + (gid & 3) * (RJ == 1 ? 2 : 8) + (RJ == 1 ? 0 : (tid & 1) * 4);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        uint32_t a[4][3];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int h = 2 * (e >> 1), t = at[2 * m + (e & 1)];
-          split3(ok[h] ? __ldg(row[h] + t) : 0.f, ok[h + 1] ? __ldg(row[h + 1] + t) : 0.f, a[e]);
+        const float* c = w[m][i];
+        const float x0 = c[0] * f0, y0 = c[2] * f0, x1 = c[1] * f1, y1 = c[3] * f1;
+        uint4 v;                                               // (high, low) of two receivers
+        v.x = pack_f16(x0, y0), v.z = pack_f16(x1, y1);
+        const float2 b0 = unpack_f16(v.x), b1 = unpack_f16(v.z);
+        v.y = pack_f16(x0 - b0.x, y0 - b0.y), v.w = pack_f16(x1 - b1.x, y1 - b1.y);
+        uint32_t* to = rec + (m >> 1) * (RJ * kBlock) + ((m & 1) * 2 + (gid >> 2)) * (RJ * 8);
+        if (RJ == 1) {
+          *reinterpret_cast<uint2*>(to) = make_uint2(v.x, v.y);
+          if (un + 1 < p.units) *reinterpret_cast<uint2*>(to + (int64_t)n * kBlock) = make_uint2(v.z, v.w);
+        } else {
+          *reinterpret_cast<uint4*>(to) = v;
         }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          constexpr int part[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
-#pragma unroll
-          for (int e = 0; e < 6; ++e) {
-            const int x = part[e][0], y = part[e][1];
-            mma_bf16(w[m][i], a[0][x], a[1][x], a[2][x], a[3][x], wb[i][0][y], wb[i][1][y]);
-          }
-        }
-      }
-    }
-    if (j0 + kWeightTokens > ctx) {
-      // a weight of a token that does not exist is 0, whatever W holds
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j + 16 * m + 4 * (e >> 1) >= ctx) {
-#pragma unroll
-            for (int i = 0; i < NT; ++i) w[m][i][e] = 0.f;
-          }
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {                          // column 2 tid + e
-        uint32_t m = 0;
-#pragma unroll
-        for (int k = 0; k < MT; ++k)
-          m = max(m, max(__float_as_uint(w[k][i][e]) & 0x7fffffffu, __float_as_uint(w[k][i][e + 2]) & 0x7fffffffu));
-#pragma unroll
-        for (int x = 4; x < 32; x *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, x));
-        if (gid == 0) atomicMax(&max_s[8 * i + 2 * tid + e], m);
-      }
-  }
-  __syncthreads();
-  if (!live) return;
-  // infinities and NaN stay what they are
-  auto power = [&](int k) {
-    const uint32_t m = max_s[k];
-    return m == 0 || m >= 0x7f800000u ? 0 : min(13 - ((int)(m >> 23) - 127), 126);
-  };
-  if (threadIdx.x < kWeightSlots && u0 + threadIdx.x / RJ < p.units)
-    p.powers[(((int64_t)b * p.units + u0 + threadIdx.x / RJ) * p.chunks + chunk) * RJ + threadIdx.x % RJ] =
-        power(threadIdx.x);
-  const int n = p.chunks * (kChunk / kBlock), block = j0 / kBlock;
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const float f0 = pow2i(power(8 * i + 2 * tid)), f1 = pow2i(power(8 * i + 2 * tid + 1));
-    const int un = u0 + (8 * i + 2 * tid) / RJ;
-    if (un >= p.units) continue;
-    uint32_t* rec = reinterpret_cast<uint32_t*>(p.records) + (((int64_t)b * p.units + un) * n + block) * (RJ * kBlock) +
-                    (RJ == 8 ? (tid >> 1) * 32 : 0) + (gid & 3) * (RJ == 1 ? 2 : 8) + (RJ == 1 ? 0 : (tid & 1) * 4);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const float* c = w[m][i];
-      const float x0 = c[0] * f0, y0 = c[2] * f0, x1 = c[1] * f1, y1 = c[3] * f1;
-      uint4 v;                                               // (high, low) of two receivers
-      v.x = pack_f16(x0, y0), v.z = pack_f16(x1, y1);
-      const float2 b0 = unpack_f16(v.x), b1 = unpack_f16(v.z);
-      v.y = pack_f16(x0 - b0.x, y0 - b0.y), v.w = pack_f16(x1 - b1.x, y1 - b1.y);
-      uint32_t* to = rec + (m >> 1) * (RJ * kBlock) + ((m & 1) * 2 + (gid >> 2)) * (RJ * 8);
-      if (RJ == 1) {
-        *reinterpret_cast<uint2*>(to) = make_uint2(v.x, v.y);
-        if (un + 1 < p.units) *reinterpret_cast<uint2*>(to + (int64_t)n * kBlock) = make_uint2(v.z, v.w);
-      } else {
-        *reinterpret_cast<uint4*>(to) = v;
       }
     }
   }
@@ -484,7 +505,9 @@ size_t mapped_shape(int batch, int H_kv, int group, int d, int max_ctx, MappedPa
 template <int RJ>
 int launch_weights(const MappedParams& p, cudaStream_t st) {
   constexpr int UN = kWeightSlots / RJ;
-  quant_weights_kernel<RJ><<<dim3((p.units + UN - 1) / UN, p.batch, p.chunks), kWeightThreads, 0, st>>>(p);
+  const int slices = (p.units + UN - 1) / UN;
+  const int64_t items = (int64_t)slices * p.batch * p.chunks;
+  quant_weights_kernel<RJ><<<(unsigned int)std::min<int64_t>(items, 148 * 2), kWeightThreads, 0, st>>>(p, slices);
   IAMAP_LAUNCH_CHECK("quant_weights_kernel");
   return IAMAP_OK;
 }
