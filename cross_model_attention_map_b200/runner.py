@@ -285,7 +285,7 @@ class QuantSenderRows:
         dev = self.rows.device
         _expect("q", q, torch.bfloat16, (self.batch, self.H_s, self.d), dev)
         _expect("ctx_lens", ctx_lens, torch.int32, (self.batch,), dev)
-        _same_cache(cache, self.H_k, self.d)
+        _same_cache(cache, self.H_k, self.d, dev)
         max_pages = cache._table(page_table, self.batch)
         C.iamap_sender_rows_quant(q, cache.codes, cache.scales, cache.num_pages, page_table,
                                   max_pages, cache.page_size, ctx_lens, self.max_ctx,
@@ -312,7 +312,7 @@ class QuantDecodeStep:
         _expect("p_rows", p_rows, torch.float32, (self.batch, self.H_s, self.ctx_stride), dev)
         _expect("W", W, torch.float32, (self.H_r, self.H_s), dev)
         _expect("ctx_lens", ctx_lens, torch.int32, (self.batch,), dev)
-        _same_cache(cache, self.H_kv, self.d_v)
+        _same_cache(cache, self.H_kv, self.d_v, dev)
         max_pages = cache._table(page_table, self.batch)
         C.iamap_mapped_av_paged_quant(p_rows, self.ctx_stride, W, cache.codes, cache.scales,
                                       cache.num_pages, page_table, max_pages,
@@ -339,8 +339,8 @@ class QuantAttention:
         dev = self.out.device
         _expect("q", q, torch.bfloat16, (self.batch, self.H_q, self.d), dev)
         _expect("ctx_lens", ctx_lens, torch.int32, (self.batch,), dev)
-        _same_cache(k_cache, self.H_kv, self.d)
-        _same_cache(v_cache, self.H_kv, self.d)
+        _same_cache(k_cache, self.H_kv, self.d, dev)
+        _same_cache(v_cache, self.H_kv, self.d, dev)
         if k_cache.num_pages != v_cache.num_pages or k_cache.page_size != v_cache.page_size:
             raise ValueError("keys and values must share their pages")
         max_pages = k_cache._table(page_table, self.batch)
@@ -353,10 +353,10 @@ class QuantAttention:
         return self.out if self.lse is None else (self.out, self.lse)
 
 
-def _same_cache(cache, H, d):
-    if cache.H != H or cache.d != d:
-        raise ValueError("a cache of %d heads of %d expected, got %d of %d" % (H, d, cache.H,
-                                                                              cache.d))
+def _same_cache(cache, H, d, device):
+    if cache.H != H or cache.d != d or cache.device != device:
+        raise ValueError("a cache of %d heads of %d on %s expected, got %d of %d on %s" % (
+            H, d, device, cache.H, cache.d, cache.device))
 
 
 class HeadMatch:

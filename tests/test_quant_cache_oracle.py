@@ -190,3 +190,18 @@ def test_runner_refusals(lib):
     empty = QuantCache(3, 16, 2, 64, 4, device="cpu")
     from oracle import quant_cache as Q
     assert not Q.values(empty.codes.numpy(), empty.scales.numpy(), 4).any()
+
+
+def test_runner_refuses_a_cache_on_another_device(lib):
+    from cross_model_attention_map_b200.runner import (QuantAttention, QuantCache, QuantDecodeStep,
+                                                       QuantSenderRows)
+    ck = QuantCache(1, 16, 2, 64, 4, device="cpu")
+    meta = lambda *shape, t=torch.float32: torch.empty(*shape, dtype=t, device="meta")  # noqa: E731
+    q, lens = meta(1, 2, 64, t=torch.bfloat16), meta(1, t=torch.int32)
+    table = torch.zeros(1, 1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="on meta expected"):
+        QuantSenderRows(1, 2, 64, 16, device="meta").run(q, ck, table, lens)
+    with pytest.raises(ValueError, match="on meta expected"):
+        QuantDecodeStep(1, 2, 2, 64, 16, device="meta").run(meta(1, 2, 16), meta(2, 2), ck, table, lens)
+    with pytest.raises(ValueError, match="on meta expected"):
+        QuantAttention(1, 2, 64, 16, device="meta").run(q, ck, ck, table, lens)
