@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheIoParam
 
 int cache_io_check(const void* rows, const int32_t* cu, const int32_t* starts, int num_seqs,
                    int64_t n) {
-  if (!rows || !cu || !starts) return set_error(IAMAP_ERR_INVALID_ARG, "null pointer");
+  if ((n != 0 && !rows) || !cu || !starts) return set_error(IAMAP_ERR_INVALID_ARG, "null pointer");
   if (num_seqs < 1 || n < 0 || n > 0x7fffffff)
     return set_error(IAMAP_ERR_INVALID_ARG, "need num_seqs >= 1 and 0 <= n < 2^31");
   if ((reinterpret_cast<uintptr_t>(rows) & 15u) != 0)

@@ -247,7 +247,8 @@ class QuantCache:
         shape, stride = x.shape, x.stride()
         n, width = shape[0], self.H * self.d
         packed = ((shape[1:] == (width,) and stride[1:] == (1,))
-                  or (shape[1:] == (self.H, self.d) and stride[1:] == (self.d, 1)))
+                  or (shape[1:] == (self.H, self.d) and stride[2] == 1
+                      and (self.H == 1 or stride[1] == self.d)))
         if x.dtype is not torch.bfloat16 or x.device != self.device or not (packed or n == 0):
             raise ValueError("x must be bf16 [n, H, d] or [n, H * d] on %s with packed rows"
                              % self.device)

@@ -157,6 +157,25 @@ def test_write_then_read(C, bits, d, page, H):
     assert bool((out[len(ref):] == 7.0).all())
 
 
+def test_one_head_and_no_rows(C):
+    """A single head's rows may carry any stride in the head's place; an empty batch does nothing."""
+    from cross_model_attention_map_b200.runner import QuantCache
+    ck = QuantCache(2, 16, 1, 64, 8)
+    x = torch.randn(1, 20, 64, device="cuda").bfloat16().transpose(0, 1)
+    assert x.stride()[1] == 20 * 64
+    table = i32([[1, 0]])
+    ck.write(x, i32([0, 20]), i32([0]), table)
+    a = ck.read(i32([0, 20]), i32([0]), table, torch.empty(20, 1, 64, dtype=torch.bfloat16, device="cuda"))
+    # half a step of the scale (at most max |x| / 127 and an fp16 rounding), then a bf16 rounding
+    assert float((a.float() - x.float()).abs().max()) <= float(x.float().abs().max()) * (0.501 / 127 + 2.0 ** -8)
+    before = ck.codes.clone()
+    none = torch.empty(0, 1, 64, dtype=torch.bfloat16, device="cuda")
+    ck.write(none, i32([0, 0]), i32([0]), table)
+    assert ck.read(i32([0, 0]), i32([0]), table, none) is none
+    torch.cuda.synchronize()
+    assert torch.equal(ck.codes, before) and C.iamap_device_status() == 0
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 def test_every_bf16_quotient_near_a_border(C, bits):
     """Codes are decided by exact comparisons: rows whose elements lie at, and one bf16 step beside,
@@ -265,6 +284,7 @@ def check_rows(got, q, pool, scales, bits, table, lens, page):
     ([4100, 2049], 14, 14, 64, 32, 0),
     ([9001], 9, 1, 128, 24, 0),
     ([33000, 5], 7, 1, 64, 64, 11),
+    ([500, 0, 37], 3, 3, 64, 16, 1700),
 ])
 def test_rows(C, bits, lens, H_s, H_k, d, page, extra):
     from cross_model_attention_map_b200.runner import QuantSenderRows
@@ -356,6 +376,9 @@ def check_mapped(got, p, W, pool, scales, bits, table, lens, page):
     ([5000, 77], 2, 34, 2, 64, 32, 0),
     ([700], 128, 128, 128, 64, 16, 0),
     ([90, 33], 1, 128, 2, 64, 64, 3),
+    # more sequences than a warp has lanes, groups of 32 of them empty, more ranges than CTAs
+    ([0] * 40 + [n * 97 % 1300 for n in range(50)] + [0] * 70 + [700, 0], 14, 64, 64, 64, 16, 0),
+    ([3, 0, 513] * 14 + [1025], 17, 6, 2, 128, 16, 0),
 ])
 def test_mapped(C, bits, lens, S, H, H_kv, d, page, extra):
     """Rows past a sequence's length hold NaN: they are not used."""

@@ -205,3 +205,8 @@ def test_runner_refuses_a_cache_on_another_device(lib):
         QuantDecodeStep(1, 2, 2, 64, 16, device="meta").run(meta(1, 2, 16), meta(2, 2), ck, table, lens)
     with pytest.raises(ValueError, match="on meta expected"):
         QuantAttention(1, 2, 64, 16, device="meta").run(q, ck, ck, table, lens)
+
+
+def test_no_rows(lib):
+    """An empty tensor has no address."""
+    assert _write(lib, n=0, x=None) == 0 and _read(lib, n=0, out=None) == 0
