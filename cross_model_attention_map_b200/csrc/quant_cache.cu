@@ -7,8 +7,8 @@
 // instructions for every 8 elements of 32 lanes, so: a lane holds half a group (the scale, its reciprocal
 // and the addresses serve 16 elements), a quotient is one fused multiply-add and one addition, and a CTA
 // looks its tokens' places up once, while its loads are in flight. 40960 tokens of 40 heads of 128 in 4
-// bits, written and read back: @@ us of 1.07 GB (8 elements a lane with IEEE divisions and a lookup a
-// lane: 693 us; without those 361 us).
+// bits, written and read back: 220 us for 1.07 GB, 4.9 TB/s (8 elements a lane with IEEE divisions and a
+// lookup a lane: 693 us; without those 361 us).
 #include <algorithm>
 
 #include "internal.h"

@@ -2,13 +2,14 @@
 //
 //   out[b, r] = sum_{j < ctx[b]} w[r, j] v^[b, j, r / group],  w[r, j] = sum_s W[r, s] p[b, s, j]
 //
-// Bound by the value bytes (72 a token and head of 128 in 4 bits). A first kernel forms the weights w (a
-// few per cent of the work) and leaves them in the workspace; then a CTA takes a range of tokens of one
-// sequence and up to eight units, a unit being a value head with up to eight of the receiver heads that
-// read it, and each warp streams the tokens of one unit with their weights through a ring of copies, 64
-// (or 32) at a time. No barrier stands in the loop. (Weights formed by the CTA for its whole range,
-// between barriers, and by every warp for each step, were slower: 104 and 125 us where this takes @@,
-// grouped ragged in 8 bits.)
+// Bound by the value bytes (72 a token and head of 128 in 4 bits). A first kernel forms the weights w and
+// leaves them in the workspace; then a CTA takes a range of tokens of one sequence and up to eight units, a
+// unit being a value head with up to eight of the receiver heads that read it, and each warp streams the
+// tokens of one unit with their weights through a ring of copies, 64 (or 32) at a time. No barrier stands
+// in the loop. Twelve ragged sequences of up to 32768 tokens, 14 rows to 64 heads over 8 value heads of 128
+// in 8 bits: 62 us, the weights 19 of them (weights formed by the CTA for its whole range, between barriers:
+// 104; by every warp for each step: 125). Four of 8704 tokens, 64 value heads in 4 bits: 56 us (62 with
+// 32 tokens a step and three CTAs an SM).
 //
 // The product runs on matrix instructions with the codes as one operand (quant_tile.cuh). Its other
 // operand, the weight times the token's scale of the group, has to keep fp32's precision in fp16, so it
@@ -18,9 +19,10 @@
 //
 // which leaves an error of 2^-22 relative, or 2^-25 absolute: the first kernel brings the largest |w| of
 // each receiver and 512 tokens, which is what a range holds, into [2^13, 2^14), so the absolute part is far
-// below the largest products. Scales of 2 and more are taken times a power of two of the warp's own (2^-E), found when one
-// comes. With one receiver a value head (group 1), the eight columns are the (group of 32, part) pairs, and
-// one operand serves all groups; otherwise they are (receiver, part) and the operand is formed a group.
+// below the largest products. Scales of 2 and more are taken times a power of two of the warp's own (2^-E),
+// found when one comes. With one receiver a value head (group 1), the eight columns are the (group of 32,
+// part) pairs, and one operand serves all groups; otherwise they are (receiver, part) and the operand is
+// formed a group.
 //
 // Partial sums of the ranges go to the workspace; a third kernel adds them in a fixed order.
 #include <algorithm>
@@ -83,9 +85,10 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 // the order in which a warp's lanes want them.
 //
 // The weights: a CTA a range of tokens for sixteen receivers, a warp 64 of the tokens. The products run on
-// matrix instructions with both factors in three bf16 parts; the six products of the larger parts leave an
-// error of 2^-25 relative, below fp32's rounding. (fp32 arithmetic, eight receivers a CTA: 28 us where this
-// takes @@, 118 thousand tokens, 14 rows to 64 heads.)
+// matrix instructions with both factors in three bf16 parts, of 2^-8 and 2^-17 of the first at most; the six
+// products of the larger parts leave out 1.5 x 2^-24 of a product, fp32's own rounding. (fp32 arithmetic,
+// eight receivers a CTA: 28 us where this takes 19, 118 thousand tokens, 14 rows to 64 heads; a CTA for
+// every range up to max_ctx, most of them behind a sequence's end: 24.)
 constexpr int kWeightSlots = 16, kWeightTokens = 64, kWeightThreads = kChunk / kWeightTokens * 32;
 template <int RJ>
 __global__ void __launch_bounds__(kWeightThreads, 2) quant_weights_kernel(const MappedParams p, int slices) {
@@ -128,14 +131,14 @@ __global__ void __launch_bounds__(kWeightThreads, 2) quant_weights_kernel(const 
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[m][i][e] = 0.f;
     if (live) {
-      const float* W[NT];                                      // column gid's row of W
+      const float* W[NT];                                    // column gid's row of W
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const int k = 8 * i + gid, un = u0 + k / RJ, of = un % p.rtiles * p.rj + k % RJ;
         const bool ok = un < p.units && k % RJ < p.rj && of < p.group;
         W[i] = ok ? p.W + ((int64_t)(un / p.rtiles) * p.group + of) * p.H_s : nullptr;
       }
-      int at[2 * MT];                                          // tokens that do not exist read the last one's row
+      int at[2 * MT];                                        // tokens that do not exist read the last one's row
 #pragma unroll
       for (int m = 0; m < 2 * MT; ++m) at[m] = min(j + 16 * (m >> 1) + 4 * (m & 1), ctx - 1);
       for (int s0 = 0; s0 < p.H_s; s0 += 16) {
@@ -192,7 +195,8 @@ __global__ void __launch_bounds__(kWeightThreads, 2) quant_weights_kernel(const 
           uint32_t m = 0;
 #pragma unroll
           for (int k = 0; k < MT; ++k)
-            m = max(m, max(__float_as_uint(w[k][i][e]) & 0x7fffffffu, __float_as_uint(w[k][i][e + 2]) & 0x7fffffffu));
+            m = max(m, max(__float_as_uint(w[k][i][e]) & 0x7fffffffu,
+                         __float_as_uint(w[k][i][e + 2]) & 0x7fffffffu));
 #pragma unroll
           for (int x = 4; x < 32; x *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, x));
           if (gid == 0) atomicMax(&max_s[now][8 * i + 2 * tid + e], m);
@@ -215,7 +219,8 @@ __global__ void __launch_bounds__(kWeightThreads, 2) quant_weights_kernel(const 
       const float f0 = pow2i(power(8 * i + 2 * tid)), f1 = pow2i(power(8 * i + 2 * tid + 1));
       const int un = u0 + (8 * i + 2 * tid) / RJ;
       if (un >= p.units) continue;
-      uint32_t* rec = reinterpret_cast<uint32_t*>(p.records) + (((int64_t)b * p.units + un) * n + block) * (RJ * kBlock) +
+      uint32_t* rec = reinterpret_cast<uint32_t*>(p.records) +
+                      (((int64_t)b * p.units + un) * n + block) * (RJ * kBlock) +
                       (RJ == 8 ? (tid >> 1) * 32 : 0) + (gid & 3) * (RJ == 1 ? 2 : 8) + (RJ == 1 ? 0 : (tid & 1) * 4);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {

@@ -594,8 +594,11 @@ int iamap_prefix_lookup(const uint64_t* keys, int64_t count, const int64_t* key_
  * launch, so a captured graph may be replayed with other lengths up to max_ctx. A length outside
  * [0, max_ctx] is clamped and sets IAMAP_DEV_BAD_INDEX. A page index outside [0, num_pages) makes
  * its tokens count as absent (probability or contribution 0) and sets IAMAP_DEV_BAD_INDEX.
- * A workspace belongs to one call in flight: calls that may overlap on the GPU, captured graphs
- * among them, need one each.
+ * A workspace (16-byte aligned) belongs to one call in flight: calls that may overlap on the GPU,
+ * captured graphs among them, need one each; nothing in it is kept from one call for the next.
+ * Limits (beyond them IAMAP_ERR_UNSUPPORTED): num_pages * H * page_size < 2^32, batch <= 65535,
+ * max_ctx <= 2^30. Pages of a multiple of 16 tokens are read in whole tiles; any other page_size
+ * works, row by row and slower.
  * ------------------------------------------------------------------------------------------- */
 
 /*
@@ -603,8 +606,8 @@ int iamap_prefix_lookup(const uint64_t* keys, int64_t count, const int64_t* key_
  *   x       bf16, row i's head h at x + i * x_stride + h * d (x_stride in elements, a multiple of 8,
  *           at least H * d: a slice of a fused projection's output needs no copy); 16-byte aligned
  *   n       rows of x; row cu[s] + i of sequence s (device int32 cu [num_seqs + 1]) becomes token
- *           starts[s] + i (device int32 [num_seqs]). Rows outside [cu[0], cu[num_seqs]) (a padded
- *           batch) are ignored.
+ *           starts[s] + i (device int32 [num_seqs], num_seqs >= 1). Rows outside
+ *           [cu[0], cu[num_seqs]) (a padded batch) are ignored. n = 0 does nothing.
  * A row whose token lies outside the page table, or whose page index is outside [0, num_pages), is
  * not stored and sets IAMAP_DEV_BAD_INDEX. The slots that one call writes must be distinct (rows of
  * two sequences must not share a slot). Only those slots' bytes change. Asynchronous on stream.
@@ -646,7 +649,10 @@ int iamap_sender_rows_quant(const void* q, const void* k_codes, const void* k_sc
  *   out[b, r, :] = sum_{j < ctx_lens[b]} (sum_s W[r, s] * p_rows[b, s, j]) * v[b, j, r / (H_r / H_kv), :]
  * p_rows fp32 [batch, H_s, ctx_stride] (entries at j >= ctx_lens[b] are not used), W fp32
  * [H_r, H_s], out fp32 [batch, H_r, d_v] (16-byte aligned). H_s, H_r <= 128; H_kv divides H_r.
- * ws: iamap_mapped_av_paged_quant_workspace_bytes bytes.
+ * Precision is that of fp32 sums; entries of p_rows or W beyond bf16's range (3.38e38) count as
+ * infinite, and a sum that meets an infinity or NaN is not finite.
+ * ws: iamap_mapped_av_paged_quant_workspace_bytes bytes (the weights, 4 bytes a token of max_ctx
+ * and receiver head, and the partial sums of each 512 tokens).
  */
 size_t iamap_mapped_av_paged_quant_workspace_bytes(int batch, int H_r, int d_v, int max_ctx);
 int iamap_mapped_av_paged_quant(const float* p_rows, int ctx_stride, const float* W,
