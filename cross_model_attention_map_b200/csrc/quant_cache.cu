@@ -18,7 +18,8 @@ namespace iamap {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 2;         // half-groups in flight a thread
+constexpr int kUnroll = 2;         // half-groups in flight a thread that writes
+constexpr int kReadUnroll = 4;     // one that reads
 constexpr int kMaxTokens = 128;    // tokens a CTA
 
 // A row's place: the pool row of its head 0 (head h: h * page_size rows further), or
@@ -223,12 +224,12 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheIoParam
   find_places(p, i0, place);
   __syncthreads();
   __nv_bfloat16* out0 = p.out + i0 * (int64_t)p.per * 16;
-  for (int base = 0; base < units; base += kThreads * kUnroll) {
-    uint32_t w[kUnroll][W];
-    uint16_t sb[kUnroll];
-    int64_t at[kUnroll];
+  for (int base = 0; base < units; base += kThreads * kReadUnroll) {
+    uint32_t w[kReadUnroll][W];
+    uint16_t sb[kReadUnroll];
+    int64_t at[kReadUnroll];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
+    for (int k = 0; k < kReadUnroll; ++k) {
       const int c = base + threadIdx.x + k * kThreads;
       const int tok = p.tokens == 1 ? 0 : (int)__umulhi((uint32_t)c, p.per_inv);
       at[k] = c < units ? place[tok] : kNoToken;
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheIoParam
       }
     }
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
+    for (int k = 0; k < kReadUnroll; ++k) {
       const int c = base + threadIdx.x + k * kThreads;
       if (c - lane >= units) break;                          // the whole warp
       const float s = __half2float(__ushort_as_half(sb[k]));

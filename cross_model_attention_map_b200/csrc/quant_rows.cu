@@ -150,31 +150,45 @@ __global__ void __launch_bounds__(kThreads, 5) quant_rows_kernel(const RowsParam
   }
 }
 
-constexpr int kNormTokens = 2048;    // tokens a CTA of the second kernel
-__global__ void __launch_bounds__(256) quant_rows_norm_kernel(RowsParams p, int parts) {
+// The second kernel: a CTA normalises 2048 tokens of a row. Its logits are under way before the ranges'
+// (reference, sum) pairs are joined, which every warp does by itself (read after the join, one at a time,
+// they made this kernel as long as the first).
+constexpr int kNormTokens = 2048, kNormThreads = 256;
+__global__ void __launch_bounds__(kNormThreads) quant_rows_norm_kernel(RowsParams p, int parts) {
+  constexpr int N = kNormTokens / kNormThreads;
   const int part = blockIdx.x % parts;
   const int64_t r = blockIdx.x / parts;                    // row b * Hq + h
   const int ctx = min(max(p.ctx_lens[r / p.Hq], 0), p.max_ctx);
   const int n = (ctx + p.chunk - 1) / p.chunk;
-  const float2* ml = p.ml + r * p.splits;
+  const int lane = threadIdx.x & 31, j0 = part * kNormTokens + threadIdx.x;
+  float* row = p.rows + r * p.stride;
   after_previous();
-  __shared__ float lse_s;
-  if (threadIdx.x < 32) {
-    float m = kNoRef, z = 0.f;
-    for (int s = threadIdx.x; s < n; s += 32) m = fmaxf(m, ml[s].x);
+  float x[N];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int s = threadIdx.x; s < n; s += 32) z = fmaf(ml[s].y, ex2(ml[s].x - m), z);
+  for (int k = 0; k < N; ++k) x[k] = j0 + k * kNormThreads < ctx ? row[j0 + k * kNormThreads] : 0.f;
+  float lse = INFINITY;
+  if (part * kNormTokens < ctx) {
+    const float2* ml = p.ml + r * p.splits;
+    float m = kNoRef, z = 0.f;
+    for (int s = lane; s < n; s += 32) {
+      const float2 v = ml[s];
+      const float top = fmaxf(m, v.x);
+      z = z * ex2(m - top) + v.y * ex2(v.x - top);
+      m = top;
+    }
+    float top = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    z *= ex2(m - top);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    if (threadIdx.x == 0) lse_s = z == 0.f ? INFINITY : m + log2f(z);
+    if (z != 0.f) lse = top + log2f(z);
   }
-  __syncthreads();
-  const float lse = lse_s;
-  float* row = p.rows + r * p.stride;
-  const int end = min(p.stride, (part + 1) * kNormTokens);
-  for (int j = part * kNormTokens + threadIdx.x; j < end; j += 256)
-    row[j] = j < ctx && lse != INFINITY ? ex2(row[j] - lse) : 0.f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int j = j0 + k * kNormThreads;
+    if (j < p.stride) row[j] = j < ctx && lse != INFINITY ? ex2(x[k] - lse) : 0.f;
+  }
 }
 
 void rows_split(int units, int max_ctx, int* chunk, int* splits) {
@@ -201,7 +215,7 @@ int launch_d(const RowsParams& p, int bits, cudaStream_t st) {
   if (p.single) return IAMAP_OK;
   const int parts = (p.stride + kNormTokens - 1) / kNormTokens;
   return launch_next("quant_rows_norm_kernel", quant_rows_norm_kernel,
-                     dim3((unsigned int)((int64_t)p.batch * p.Hq * parts)), 256, 0, st, p, parts);
+                     dim3((unsigned int)((int64_t)p.batch * p.Hq * parts)), kNormThreads, 0, st, p, parts);
 }
 
 }  // namespace
