@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 2;         // half-groups in flight a thread that writes
-constexpr int kReadUnroll = 4;     // one that reads
+constexpr int kReadUnroll = 3;     // one that reads
 constexpr int kMaxTokens = 128;    // tokens a CTA
 
 // A row's place: the pool row of its head 0 (head h: h * page_size rows further), or
