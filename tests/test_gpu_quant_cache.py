@@ -285,6 +285,8 @@ def check_rows(got, q, pool, scales, bits, table, lens, page):
     ([9001], 9, 1, 128, 24, 0),
     ([33000, 5], 7, 1, 64, 64, 11),
     ([500, 0, 37], 3, 3, 64, 16, 1700),
+    ([500, 0, 37], 3, 3, 64, 16, 3700),
+    ([4096, 4097, 0], 2, 1, 64, 16, 0),
 ])
 def test_rows(C, bits, lens, H_s, H_k, d, page, extra):
     from cross_model_attention_map_b200.runner import QuantSenderRows
