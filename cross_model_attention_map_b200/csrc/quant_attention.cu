@@ -288,53 +288,51 @@ __global__ void __launch_bounds__(kThreads, 4) quant_attention_kernel(const Attn
   }
 }
 
-// Joins the ranges of one query head: eight warps (sixteen halves of them for D = 64) take a range each in
-// turn, then their sums are added in a fixed order. (One thread an element over all ranges took 21 us for
-// one sequence of 131071 tokens, mostly latency.)
-constexpr int kJoinThreads = 256;
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) quant_attention_join_kernel(AttnParams p) {
-  constexpr int L = D / 4, G = kJoinThreads / L;             // lanes a range, ranges at a time
+// Joins the ranges of one query head: a warp (half of one for D = 64) takes a range in turn and keeps its own
+// running reference, sum and output, then these are added in a fixed order. T = 256 threads, or 1024 where
+// there are more than 32 ranges. (One thread an element over all ranges took 21 us for one sequence of
+// 131071 tokens, mostly latency; the largest reference looked up first, and 256 threads for its 74 ranges, 9.)
+template <int D, int T>
+__global__ void __launch_bounds__(T) quant_attention_join_kernel(AttnParams p) {
+  constexpr int L = D / 4, G = T / L;                        // lanes a range, ranges at a time
   const int h = blockIdx.x % p.Hq, b = blockIdx.x / p.Hq;
   const int ctx = min(max(p.ctx_lens[b], 0), p.max_ctx);
-  after_previous();
   const int nsplit = (ctx + p.chunk - 1) / p.chunk;
-  if (nsplit <= 1) return;
   const int hk = h / p.group, hg = h - hk * p.group;
   const int64_t unit = ((int64_t)b * p.k.H + hk) * p.htiles + hg / kHeads;
   const int64_t first = unit * p.splits * p.hpu + hg % kHeads;
-  __shared__ float red[kJoinThreads / 32];
-  __shared__ float z_s[G];
+  __shared__ float2 mz_s[G];
   __shared__ __align__(16) float a_s[G][D];
-  float m = kNoRef;
-  for (int s = threadIdx.x; s < nsplit; s += kJoinThreads)
-    m = fmaxf(m, p.ml[first + (int64_t)s * p.hpu].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w]);
+  after_previous();
+  if (nsplit <= 1) return;
   const int g = threadIdx.x / L, e = threadIdx.x % L * 4;
-  float z = 0.f;
+  float m = kNoRef, z = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int s = g; s < nsplit; s += G) {
     const int64_t part = first + (int64_t)s * p.hpu;
     const float2 ml = p.ml[part];
     const float4 x = *reinterpret_cast<const float4*>(p.acc + part * D + e);
-    const float f = ex2(ml.x - m);
-    z = fmaf(ml.y, f, z);
-    a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y), a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
+    const float top = fmaxf(m, ml.x), old = ex2(m - top), f = ex2(ml.x - top);
+    m = top;
+    z = fmaf(ml.y, f, z * old);
+    a.x = fmaf(x.x, f, a.x * old), a.y = fmaf(x.y, f, a.y * old);
+    a.z = fmaf(x.z, f, a.z * old), a.w = fmaf(x.w, f, a.w * old);
   }
   *reinterpret_cast<float4*>(&a_s[g][e]) = a;
-  if (e == 0) z_s[g] = z;
+  if (e == 0) mz_s[g] = make_float2(m, z);
   __syncthreads();
   if (threadIdx.x >= D) return;
+  m = kNoRef;
+#pragma unroll 8
+  for (int k = 0; k < G; ++k) m = fmaxf(m, mz_s[k].x);
   float sum = 0.f;
   z = 0.f;
-#pragma unroll
-  for (int k = 0; k < G; ++k) sum += a_s[k][threadIdx.x], z += z_s[k];
+#pragma unroll 8
+  for (int k = 0; k < G; ++k) {
+    const float f = ex2(mz_s[k].x - m);
+    sum = fmaf(a_s[k][threadIdx.x], f, sum), z = fmaf(mz_s[k].y, f, z);
+  }
   const int64_t row = (int64_t)b * p.Hq + h;
   p.out[row * D + threadIdx.x] = __float2bfloat16(z == 0.f ? 0.f : sum / z);
   if (p.lse && threadIdx.x == 0) p.lse[row] = z == 0.f ? -INFINITY : (m + log2f(z)) * kLn2;
@@ -367,11 +365,11 @@ int launch(const AttnParams& p, cudaStream_t st) {
   const dim3 grid(p.k.H * p.htiles, p.batch, p.splits);
   quant_attention_kernel<D, KB, VB, ALIGNED><<<grid, kThreads, bytes, st>>>(p);
   IAMAP_LAUNCH_CHECK("quant_attention_kernel");
-  if (p.splits > 1) {
-    return launch_next("quant_attention_join_kernel", quant_attention_join_kernel<D>, dim3(p.batch * p.Hq),
-                       kJoinThreads, 0, st, p);
-  }
-  return IAMAP_OK;
+  if (p.splits == 1) return IAMAP_OK;
+  const dim3 rows(p.batch * p.Hq);
+  return p.splits > 32
+             ? launch_next("quant_attention_join_kernel", quant_attention_join_kernel<D, 1024>, rows, 1024, 0, st, p)
+             : launch_next("quant_attention_join_kernel", quant_attention_join_kernel<D, 256>, rows, 256, 0, st, p);
 }
 template <int D, int KB, int VB>
 int launch_a(const AttnParams& p, cudaStream_t st) {

@@ -473,6 +473,7 @@ def check_attention(got, lse, q, k, v, kb, vb, table, lens, page):
     ([2100, 999, 3], 16, 16, 128, 16),
     ([5000, 77], 34, 2, 64, 32),
     ([20000], 8, 1, 128, 64),
+    ([9000, 12], 2, 1, 64, 32),
 ])
 def test_attention(C, kb, vb, lens, H, H_kv, d, page):
     from cross_model_attention_map_b200.runner import QuantAttention
