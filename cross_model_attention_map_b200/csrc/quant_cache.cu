@@ -118,33 +118,43 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const CacheIoP
   const int units = p.tokens * p.per;
   const int lane = threadIdx.x & 31, l = threadIdx.x % L, g = l >> 1, h = l & 1;
   const __nv_bfloat16* x0 = p.x + i0 * p.x_stride;
-  for (int base = 0; base < units; base += kThreads * kUnroll) {
-    uint32_t w[kUnroll][8];
-    int tok[kUnroll], rest[kUnroll];
+  auto half = [&](int c, int* tok, int* rest) {
+    *tok = p.tokens == 1 ? 0 : (int)__umulhi((uint32_t)c, p.per_inv);
+    *rest = c - *tok * p.per;
+  };
+  uint32_t next[kUnroll][8];
+  auto load = [&](int base) {
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
       const int c = base + threadIdx.x + k * kThreads;
-      tok[k] = p.tokens == 1 ? 0 : (int)__umulhi((uint32_t)c, p.per_inv);
-      rest[k] = c - tok[k] * p.per;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[k][e] = 0;
-      if (c < units && i0 + tok[k] < p.n) {
-        const uint4* src =
-            reinterpret_cast<const uint4*>(x0 + tok[k] * p.x_stride + 16 * rest[k] - 8 * h);
-        const uint4 a = __ldcs(src), b = __ldcs(src + 2);
-        w[k][0] = a.x, w[k][1] = a.y, w[k][2] = a.z, w[k][3] = a.w;
-        w[k][4] = b.x, w[k][5] = b.y, w[k][6] = b.z, w[k][7] = b.w;
+      int tok, rest;
+      half(c, &tok, &rest);
+      uint4 a = make_uint4(0, 0, 0, 0), b = a;
+      if (c < units && i0 + tok < p.n) {
+        const uint4* src = reinterpret_cast<const uint4*>(x0 + tok * p.x_stride + 16 * rest - 8 * h);
+        a = __ldcs(src), b = __ldcs(src + 2);
       }
+      next[k][0] = a.x, next[k][1] = a.y, next[k][2] = a.z, next[k][3] = a.w;
+      next[k][4] = b.x, next[k][5] = b.y, next[k][6] = b.z, next[k][7] = b.w;
     }
-    if (base == 0) {
-      find_places(p, i0, place);
-      __syncthreads();
-    }
+  };
+  load(0);
+  find_places(p, i0, place);
+  __syncthreads();
+  for (int base = 0; base < units; base += kThreads * kUnroll) {
+    uint32_t w[kUnroll][8];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[k][e] = next[k][e];
+    load(base + kThreads * kUnroll);
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
       const int c = base + threadIdx.x + k * kThreads;
       if (c - lane >= units) break;                          // the whole warp
-      const int64_t at = c < units ? place[tok[k]] : kNoToken;
+      int tok, rest;
+      half(c, &tok, &rest);
+      const int64_t at = c < units ? place[tok] : kNoToken;
       // largest magnitude by the bits: infinities and NaN compare above every finite value
       uint32_t m = 0;
 #pragma unroll
@@ -194,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const CacheIoP
       __syncwarp();
       if (at >= 0) {
         // pool row: at + head * page_size
-        const int64_t row = at + (uint32_t)(rest[k] / L) * (uint64_t)p.pages.page_size;
+        const int64_t row = at + (uint32_t)(rest / L) * (uint64_t)p.pages.page_size;
         uint8_t* to = p.codes + row * (RW * 4);
         if (BITS == 4)
           reinterpret_cast<uint2*>(to)[l] = reinterpret_cast<const uint2*>(mine)[l];
