@@ -5,10 +5,11 @@
 //
 // Both are bound by HBM: 2 + bits / 8 + 1 / 16 bytes an element. At that rate an SM has some 100
 // instructions for every 8 elements of 32 lanes, so: a lane holds half a group (the scale, its reciprocal
-// and the addresses serve 16 elements), a quotient is one fused multiply-add and one addition, and a CTA
-// looks its tokens' places up once, while its loads are in flight. 40960 tokens of 40 heads of 128 in 4
-// bits, written and read back: 220 us for 1.07 GB, 4.9 TB/s (8 elements a lane with IEEE divisions and a
-// lookup a lane: 693 us; without those 361 us).
+// and the addresses serve 16 elements), a quotient is half of a paired fused multiply-add and addition, and
+// a CTA looks its tokens' places up once, while its loads are in flight. 40960 tokens of 40 heads of 128 in
+// 4 bits, written and read back: 195 us for 1.07 GB, 5.5 TB/s; the write is 102 of them, 3 in 4 issue slots
+// taken (rows not loaded ahead and single additions: 212; 8 elements a lane with IEEE divisions and a lookup
+// a lane: 693).
 #include <algorithm>
 
 #include "internal.h"
@@ -73,6 +74,12 @@ __device__ __forceinline__ float rcp(float x) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+
 // Levels of eight elements w (bf16 pairs) under the scale whose reciprocal is r (within 1 ulp): x / s
 // rounded to even, exactly, plus the offset, in the low byte of each u. x r + 1536 is rounded to
 // multiples of 2^-13 and |x / s| < 128, so it is within 2^-13 of x / s + 1536. x has 8 significant bits and s at
@@ -82,10 +89,13 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 template <int BITS>
 __device__ __forceinline__ void levels(const uint32_t* w, float r, uint32_t* u) {
   constexpr float kOff = 12582912.f + (BITS == 4 ? 8.f : 128.f) - 1536.f;
+  const uint64_t rr = pair(r, r), add = pair(1536.f, 1536.f), off = pair(kOff, kOff);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float x = e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
-    u[e] = __float_as_uint(__fadd_rn(__fmaf_rn(x, r, 1536.f), kOff));
+  for (int e = 0; e < 4; ++e) {
+    uint64_t t;
+    asm("{ .reg .b64 t; fma.rn.f32x2 t, %1, %2, %3; add.rn.f32x2 %0, t, %4; }"
+        : "=l"(t) : "l"(pair(bf16_lo(w[e]), bf16_hi(w[e]))), "l"(rr), "l"(add), "l"(off));
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(u[2 * e]), "=r"(u[2 * e + 1]) : "l"(t));
   }
 }
 // The same where x / s may exceed Q: s is subnormal, saturated or 0.
@@ -118,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const CacheIoP
   const int units = p.tokens * p.per;
   const int lane = threadIdx.x & 31, l = threadIdx.x % L, g = l >> 1, h = l & 1;
   const __nv_bfloat16* x0 = p.x + i0 * p.x_stride;
+  const int live = (int)min((int64_t)p.tokens, p.n - i0);    // tokens that there are
   auto half = [&](int c, int* tok, int* rest) {
     *tok = p.tokens == 1 ? 0 : (int)__umulhi((uint32_t)c, p.per_inv);
     *rest = c - *tok * p.per;
@@ -127,13 +138,13 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const CacheIoP
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
       const int c = base + threadIdx.x + k * kThreads;
+      if (c - lane >= units) break;                          // the whole warp
       int tok, rest;
-      half(c, &tok, &rest);
-      uint4 a = make_uint4(0, 0, 0, 0), b = a;
-      if (c < units && i0 + tok < p.n) {
-        const uint4* src = reinterpret_cast<const uint4*>(x0 + tok * p.x_stride + 16 * rest - 8 * h);
-        a = __ldcs(src), b = __ldcs(src + 2);
-      }
+      half(c < units ? c : h, &tok, &rest);
+      // a lane past the CTA's rows reads its first one, past the last row that one; neither is stored
+      const uint4* src =
+          reinterpret_cast<const uint4*>(x0 + min(tok, live - 1) * p.x_stride + 16 * rest - 8 * h);
+      const uint4 a = __ldcs(src), b = __ldcs(src + 2);
       next[k][0] = a.x, next[k][1] = a.y, next[k][2] = a.z, next[k][3] = a.w;
       next[k][4] = b.x, next[k][5] = b.y, next[k][6] = b.z, next[k][7] = b.w;
     }
@@ -164,18 +175,19 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const CacheIoP
       // m / Q lies no nearer than 2^-15 of itself to a border of fp16's rounding unless it is a number of
       // fp16, so the product with fl(1 / Q) rounds as the quotient does
       const float top = __uint_as_float(m << 16) * (1.f / Q);
-      __half s = __float2half_rn(fminf(top, 65504.f));
-      const bool odd = m >= 0x7f80u;                         // a group with an infinity or NaN
-      if (odd) s = __ushort_as_half(0x7e00);
-      const float sf = odd ? 0.f : __half2float(s);
+      __half s = __float2half_rn(top);
+      const float sf = __half2float(s);
       uint32_t u[16];
       if (sf >= 6.103515625e-05f && top <= 65504.f) {
         const float r = rcp(sf);
         levels<BITS>(w[k], r, u);
         levels<BITS>(w[k] + 4, r, u + 8);
       } else {
-        levels_clamped<BITS>(w[k], sf, u);
-        levels_clamped<BITS>(w[k] + 4, sf, u + 8);
+        const bool odd = m >= 0x7f80u;                       // a group with an infinity or NaN
+        s = odd ? __ushort_as_half(0x7e00) : __float2half_rn(fminf(top, 65504.f));
+        const float cs = odd ? 0.f : __half2float(s);
+        levels_clamped<BITS>(w[k], cs, u);
+        levels_clamped<BITS>(w[k] + 4, cs, u + 8);
       }
       // the row's bytes meet in shared memory and leave in order, 8 or 16 a lane (stored from where they
       // are made, in pieces of 4 and 2, they took 2.2 times as long)
