@@ -57,7 +57,7 @@ struct AttnParams {
 template <int D, int KB, int VB>
 struct Ring {
   // 32 tokens a step and two stages a warp fit four CTAs an SM (three where both are 8 bits of 128). With
-  // three CTAs and 64 tokens the batch of 48 took as long and one sequence of 131071 tokens 59 us where two and 32 took 49.
+  // three CTAs and 64 tokens the batch of 48 took as long, and one sequence of 131071 tokens 59 us, not 49.
   static constexpr int kTiles = 2, kTokens = kTiles * kTok, kStages = 2;
   static constexpr int K = kTokens * D * KB / 8, V = kTokens * D * VB / 8, S = kTokens * (D / 32) * 2;
   static constexpr int kStage = K + S + V + S;           // keys' codes and scales, values'
