@@ -19,8 +19,9 @@
 //
 // Ranges of one sequence are joined by a second kernel; a sequence that fits in one range is written by
 // the first. 48 sequences of 4587 to 16384 tokens, 64 heads on 8 of 128, all in 4 bits: 161 us, 3.6 TB/s of
-// the cache; one of 131071, keys in 8 bits and values in 4: 47 us, 4.6 TB/s. What bounds it is issue: turning
-// codes into fp16 operands (integer instructions) and the matrix instructions share an issue slot.
+// the cache; one of 131071, keys in 8 bits and values in 4: 47 us, 4.6 TB/s. What bounds it is turning codes
+// into fp16 operands: 64 % of the issue slots and 58 % of the integer pipe, which the matrix instructions'
+// issue takes from as well, with four warps a scheduler.
 #include <algorithm>
 
 #include "internal.h"
