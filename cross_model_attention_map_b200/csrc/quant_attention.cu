@@ -393,6 +393,7 @@ using namespace iamap;
 extern "C" size_t iamap_attention_paged_quant_workspace_bytes(int batch, int H_q, int d,
                                                               int max_ctx) {
   if (batch < 1 || H_q < 1 || d < 1 || max_ctx < 0) return 0;
+  if (batch > 65535 || (int64_t)batch * H_q > 0x7fffff) return 0;    // refused by the call
   // the most that any grouping of the H_q heads needs: a unit is up to eight of them
   size_t most = 256;
   for (int group = 1; group <= H_q; ++group) {
@@ -431,7 +432,7 @@ extern "C" int iamap_attention_paged_quant(const void* q, const void* k_codes, c
   p.htiles = (p.group + kHeads - 1) / kHeads;
   p.hpu = std::min(p.group, kHeads);
   const int64_t units = (int64_t)batch * H_kv * p.htiles;
-  if (batch > 65535 || units > 0x7fffff || (int64_t)batch * H_q > 0x7fffffff)
+  if (batch > 65535 || (int64_t)batch * H_q > 0x7fffff)
     return set_error(IAMAP_ERR_UNSUPPORTED, "batch above 65535, or batch times heads too large");
   attention_split(batch, (int)units, max_ctx, &p.chunk, &p.splits);
   size_t ml_at = 0;

@@ -549,6 +549,7 @@ using namespace iamap;
 extern "C" size_t iamap_mapped_av_paged_quant_workspace_bytes(int batch, int H_r, int d_v,
                                                               int max_ctx) {
   if (batch < 1 || H_r < 1 || d_v < 1 || max_ctx < 0) return 0;
+  if (batch > 65535 || H_r > 128) return 0;                         // refused by the call
   // the most that any grouping of the H_r heads needs
   size_t most = 256;
   for (int group = 1; group <= H_r; ++group) {

@@ -231,6 +231,7 @@ using namespace iamap;
 
 extern "C" size_t iamap_sender_rows_quant_workspace_bytes(int batch, int H_s, int max_ctx) {
   if (batch < 1 || H_s < 1 || max_ctx < 0) return 0;
+  if (batch > 65535 || (int64_t)batch * H_s > 0x7fffff) return 0;    // refused by the call
   // the most that any grouping of the H_s heads needs
   size_t most = 256;
   for (int group = 1; group <= H_s; ++group) {
@@ -264,7 +265,7 @@ extern "C" int iamap_sender_rows_quant(const void* q, const void* k_codes, const
   p.group = H_s / H_k;
   p.htiles = (p.group + kHeads - 1) / kHeads;
   const int64_t units = (int64_t)batch * H_k * p.htiles;
-  if (batch > 65535 || units > 0x7fffff ||
+  if (batch > 65535 || (int64_t)batch * H_s > 0x7fffff ||
       (int64_t)batch * H_s * ((ctx_stride + (int64_t)kNormTokens - 1) / kNormTokens) > 0x7fffffff)
     return set_error(IAMAP_ERR_UNSUPPORTED, "batch above 65535, or batch times heads times ctx_stride too large");
   rows_split((int)units, max_ctx, &p.chunk, &p.splits);

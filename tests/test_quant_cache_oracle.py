@@ -210,3 +210,19 @@ def test_runner_refuses_a_cache_on_another_device(lib):
 def test_no_rows(lib):
     """An empty tensor has no address."""
     assert _write(lib, n=0, x=None) == 0 and _read(lib, n=0, out=None) == 0
+
+
+def test_batches_that_are_too_large(lib):
+    """Refused by the calls, and the workspace queries name no size for them."""
+    big = dict(batch=65536, ws_bytes=1 << 62)
+    for call in (_rows, _mapped, _attend):
+        assert call(lib, **big) == UNSUPPORTED, lib.iamap_last_error()
+    assert _rows(lib, batch=65535, H_s=256, ws_bytes=1 << 62) == UNSUPPORTED
+    assert _attend(lib, batch=65535, H_q=256, ws_bytes=1 << 62) == UNSUPPORTED
+    assert lib.iamap_sender_rows_quant_workspace_bytes(65536, 4, 20) == 0
+    assert lib.iamap_sender_rows_quant_workspace_bytes(65535, 1 << 30, 20) == 0
+    assert lib.iamap_mapped_av_paged_quant_workspace_bytes(65536, 4, 64, 20) == 0
+    assert lib.iamap_attention_paged_quant_workspace_bytes(65536, 4, 64, 20) == 0
+    assert lib.iamap_attention_paged_quant_workspace_bytes(65535, 1 << 30, 64, 20) == 0
+    for call in (_rows, _mapped, _attend):
+        assert call(lib, ws=A + 8) == INVALID and "16-byte" in lib.iamap_last_error()
