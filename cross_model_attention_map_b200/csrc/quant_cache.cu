@@ -172,8 +172,10 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const CacheIoP
       for (int e = 0; e < 8; ++e) m = __vmaxu2(m, w[k][e] & 0x7fff7fffu);
       m = max(m & 0xffffu, m >> 16);
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      // m / Q lies no nearer than 2^-15 of itself to a border of fp16's rounding unless it is a number of
-      // fp16, so the product with fl(1 / Q) rounds as the quotient does
+      // A normal fp16 quotient m / Q lies no nearer than 2^-15 of itself to a border of fp16's rounding unless
+      // it is a number of fp16, so the product with fl(1 / Q) rounds as the quotient does. A subnormal one can
+      // be halfway between two (91 x 2^-25 / 7): there the quotient itself is rounded, which fp32 holds exactly
+      // at such a border and on its side beside one (all finite m were compared).
       const float top = __uint_as_float(m << 16) * (1.f / Q);
       __half s = __float2half_rn(top);
       const float sf = __half2float(s);
@@ -184,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const CacheIoP
         levels<BITS>(w[k] + 4, r, u + 8);
       } else {
         const bool odd = m >= 0x7f80u;                       // a group with an infinity or NaN
-        s = odd ? __ushort_as_half(0x7e00) : __float2half_rn(fminf(top, 65504.f));
+        s = odd ? __ushort_as_half(0x7e00)
+                : __float2half_rn(fminf(__fdiv_rn(__uint_as_float(m << 16), Q), 65504.f));
         const float cs = odd ? 0.f : __half2float(s);
         levels_clamped<BITS>(w[k], cs, u);
         levels_clamped<BITS>(w[k] + 4, cs, u + 8);

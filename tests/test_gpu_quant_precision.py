@@ -1,0 +1,64 @@
+"""Precision of the quantised paged cache and of the decode operators over it where magnitudes differ widely:
+scales of every bf16 magnitude, groups of very different size in one head, a token that takes almost all
+of the weight. Against the float64 oracle (oracle/quant_cache.py).
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import quant_cache as Q
+from synth.workloads import bf16_bits, bf16_bits_to_f64
+
+from _gpu_common import bf16
+from test_gpu_quant_cache import cache, check_mapped, i32, mapped_inputs, score_tol, table_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def C():
+    from cross_model_attention_map_b200 import iamap
+    return iamap
+
+
+def pool_with(rng, rows, table, total, page, bits):
+    """Codes and scales of the float64 rows [n, H, d] of each sequence, garbage elsewhere."""
+    H, d = rows[0].shape[1:]
+    pool = rng.integers(0, 256, size=(total, H, page, d * bits // 8), dtype=np.uint8)
+    scales = rng.choice(np.array([np.nan, np.inf, 6e4], dtype=np.float16), size=(total, H, page, d // 32))
+    for b, x in enumerate(rows):
+        pos = np.arange(len(x))
+        c, s = Q.quantise(x, bits)
+        pool[table[b, pos // page], :, pos % page] = Q.pack(c, bits)
+        scales[table[b, pos // page], :, pos % page] = s
+    return pool, scales
+
+
+# ------------------------------------------------------------------------------------------------
+# Scales
+# ------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_scales_of_every_magnitude(C, bits):
+    """A group for each of the 32640 finite bf16 magnitudes: scale and codes exact, the quotients that lie
+    halfway between two subnormal fp16 numbers among them (91, 175 and 203 times 2^-25 in 4 bits)."""
+    rng = np.random.default_rng(3)
+    m = bf16_bits_to_f64(np.arange(0x7f80, dtype=np.uint16))
+    x = m[:, None] * rng.uniform(-1, 1, size=(len(m), 32))
+    x = bf16_bits_to_f64(bf16_bits(x.astype(np.float32)))
+    x[np.arange(len(m)), rng.integers(0, 32, size=len(m))] = m
+    x = x.reshape(-1, 1, 64)
+    n, page = len(x), 16
+    table = np.arange(-(-n // page), dtype=np.int32)[None]
+    ck = cache(np.zeros((table.size, 1, page, 64 * bits // 8), dtype=np.uint8),
+               np.zeros((table.size, 1, page, 2), dtype=np.float16), bits)
+    ck.write(bf16(bf16_bits(x.astype(np.float32))), i32([0, n]), i32([0]), i32(table))
+    assert C.iamap_device_status() == 0
+    c, s = Q.quantise(x, bits)
+    got = ck.scales.cpu().numpy().reshape(-1, 2)[:n]
+    bad = np.flatnonzero((got != s[:, 0]).ravel())
+    assert bad.size == 0, [(float(m[i] * 2.0 ** 25), float(got.ravel()[i]), float(s.ravel()[i])) for i in bad[:8]]
+    np.testing.assert_array_equal(Q.unpack(ck.codes.cpu().numpy().reshape(-1, 64 * bits // 8)[:n], bits), c[:, 0])
