@@ -19,8 +19,8 @@
 //
 // which leaves an error of 2^-22 relative, or 2^-25 absolute: the first kernel brings the largest |w| of
 // each receiver and 512 tokens, which is what a range holds, into [2^13, 2^14), so the absolute part is far
-// below the largest products. Scales of 2 and more are taken times a power of two of the warp's own (2^-E),
-// found when one comes. With one receiver a value head (group 1), the eight columns are the (group of 32,
+// below the largest products. The scales of a group are taken times a power of two where they are 2 and more
+// or small (ScalePowers). With one receiver a value head (group 1), the eight columns are the (group of 32,
 // part) pairs, and one operand serves all groups; otherwise they are (receiver, part) and the operand is
 // formed a group.
 //
@@ -62,10 +62,6 @@ struct MappedParams {
   unsigned int* status;
 };
 
-// 2^k for k in [-126, 127], clamped to it; larger shifts are made in two steps by the caller.
-__device__ __forceinline__ float pow2i(int k) {
-  return __uint_as_float((uint32_t)(min(max(k, -126), 127) + 127) << 23);
-}
 // x = b[0] + b[1] + b[2] in bf16, each part the rounding of what the ones before it leave, for a pair of values
 __device__ __forceinline__ void split3(float x, float y, uint32_t (&b)[3]) {
 #pragma unroll
@@ -300,8 +296,11 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
   // h' = 0, l' = h.
   const bool lo = gid & 1;
   const uint32_t own = lo ? 0xffffffffu : 0u;
-  int E = 0;                                                 // the scales are taken times 2^-E
-  uint32_t down = 0x3c003c00u;                               // 2^-E
+  ScalePowers<NG> pw;
+  pw.init();
+  uint32_t down[NG / 2];                                     // the groups' 2^-e; GM 0: all of this column's group
+#pragma unroll
+  for (int k = 0; k < NG / 2; ++k) down[k] = 0x3c003c00u;
 
   for (int i = 0; i < in.nsteps; ++i) {
     in.fill(i + ST - 1);
@@ -310,33 +309,40 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
     if (!in.take(&st, &masks)) break;
     const uint32_t scales = st + TK * R;
     const uint32_t weights = scales + TK * SB + (GM == 0 ? tid * 8 : tid * 32 + (gid >> 1) * 8);
-    // a scale of 2 or more (infinite, NaN) in the step
+    // a scale in the step that its group's power does not serve
     const uint2 all = lds64(scales + lane * 8 % (TK * SB));
-    const uint2 all2 = TK * SB > 256 ? lds64(scales + 256 + lane * 8) : make_uint2(0, 0);
-    if (__any_sync(0xffffffffu, (all.x | all.y | all2.x | all2.y) & 0x40004000u)) {
-      uint32_t m = 0;
+    const uint2 all2 = TK * SB > 256 ? lds64(scales + 256 + lane * 8) : all;
+    const uint32_t served = pw.served(all.x, 0) & pw.served(all.y, 1) & pw.served(all2.x, 0) & pw.served(all2.y, 1);
+    if (__any_sync(0xffffffffu, (served & 0x80008000u) != 0x80008000u)) {
+      uint32_t m[NG / 2] = {};
       const uint32_t q[4] = {all.x, all.y, all2.x, all2.y};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = (lane * 8 % (TK * SB) + 256 * (e >> 1) + 4 * (e & 1)) / SB % TK;   // the word's token
-        if (!((masks[t >> 5] >> (t & 31)) & 1)) continue;
-        const uint32_t v = q[e] & 0x7fff7fffu;
-        m = __vmaxu2(m, v & ~__vcmpgtu2(v, 0x7bff7bffu));     // infinities and NaN set no scale
+      for (int e = 0; e < (TK * SB > 256 ? 4 : 2); ++e) {
+        const int t = (lane * 8 % (TK * SB) + 256 * (e >> 1) + 4 * (e & 1)) / SB;        // the word's token
+        if ((masks[t >> 5] >> (t & 31)) & 1) m[e % (NG / 2)] = pw.larger(m[e % (NG / 2)], q[e]);
       }
-      m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-      const int e = m < 0x4000u ? 0 : (int)(m >> 10) - 15;    // floor(log2) of the largest scale
-      if (e > E) {
-        const float f = pow2i(E - e);
+      float f[NG];
+      pw.raise(m, f);
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
 #pragma unroll
         for (int c = 0; c < CT; ++c)
 #pragma unroll
-          for (int k = 0; k < 2 * NG; ++k)
+          for (int k = 0; k < 2 * NG; ++k)                   // GM 0: this lane's columns are group tid's
 #pragma unroll
-            for (int z = 0; z < 4; ++z) o[c][k][z] *= f;
-        E = e;
-        down = pack_f16(pow2i(-E), pow2i(-E));
+            for (int z = 0; z < 4; ++z)
+              if (GM == 0 ? tid == g : k / 2 == g) o[c][k][z] *= f[g];
+      auto half = [&](int g) { return (uint32_t)__half_as_ushort(__float2half_rn(pow2i(-pw.e(g)))); };
+#pragma unroll
+      for (int k = 0; k < NG / 2; ++k) {
+        down[k] = half(2 * k) | half(2 * k + 1) << 16;
+        if (GM == 0)
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+            if ((gid >> 1) % NG == g) down[k] = half(g) * 0x10001u;
       }
     }
+    const bool scaled = pw.any();
 #pragma unroll 1
     for (int h = 0; h < RB::kTiles / 2; ++h) {
       const uint32_t mask = masks[h];
@@ -365,12 +371,13 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
             const uint2 w = lds64(weights + h * REC + (GM == 0 ? (2 * q + k) * 32 : ((2 * q + k) * CT + c) * 128));
             hp[c][k] = w.x & own, lp[c][k] = lo ? w.y : w.x;
           }
-        if (E != 0) {
+        if (scaled) {
           if (GM == 0) {
-            sg[0] = hmul2(sg[0], down), sg[1] = hmul2(sg[1], down);
+            sg[0] = hmul2(sg[0], down[0]), sg[1] = hmul2(sg[1], down[0]);
           } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sc[k] = make_uint2(hmul2(sc[k].x, down), hmul2(sc[k].y, down));
+            for (int k = 0; k < 4; ++k)
+              sc[k] = make_uint2(hmul2(sc[k].x, down[0]), NG == 4 ? hmul2(sc[k].y, down[NG / 2 - 1]) : 0u);
           }
         }
         if (mask != 0xffffffffu) {
@@ -431,13 +438,14 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
   for (int c = 0; c < CT; ++c) {
     const int r = GM == 0 ? 0 : 4 * c + tid;
     if (r >= nrj || !live) continue;
-    const int k = j0 < j1 ? p.powers[(((int64_t)b * p.units + unit) * p.chunks + chunk) * RJ + r] - E : 0;
-    const float dn0 = pow2i(-(k / 2)), dn1 = pow2i(-(k - k / 2));
+    const int power = j0 < j1 ? p.powers[(((int64_t)b * p.units + unit) * p.chunks + chunk) * RJ + r] : 0;
     float* dst = (p.parts > 1 ? o_s + ((part * p.hs + warp % p.hs) * p.rj + r) * D : row_of(unit, r)) +
                  4 * gid;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       if (GM == 0 && tid != g) continue;
+      const int k = power - pw.e(g);
+      const float dn0 = pow2i(-(k / 2)), dn1 = pow2i(-(k - k / 2));
       const float* a = o[c][2 * g];
       const float* d = o[c][2 * g + 1];
       *reinterpret_cast<float4*>(dst + 32 * g) =

@@ -284,6 +284,56 @@ __device__ __forceinline__ uint32_t scale_pair(const uint2* sc, int g) {
   return g < 2 ? __byte_perm(sc[0].x, sc[1].x, sel) : __byte_perm(sc[0].y, sc[1].y, sel);
 }
 
+// Exact 2^k for k in [-126, 127], clamped to it; larger shifts are made in two steps by the caller.
+__device__ __forceinline__ float pow2i(int k) {
+  return __uint_as_float((uint32_t)(min(max(k, -126), 127) + 127) << 23);
+}
+
+// A power of two for each group of a warp's value scales. The groups are elements that share nothing but
+// their tokens, so a large group may not cost a small one its bits: group g's scales are taken times 2^-e[g],
+// under 2. e is 0 as long as the group's largest scale so far lies in [2^-8, 2), and otherwise brings it to
+// [1, 2), or [1/2, 1) below that range. It only rises, so a group's sums are rescaled a few times at most.
+template <int NG>
+struct ScalePowers {
+  uint32_t held;                   // e[g] in byte g
+  uint32_t limit[NG / 2];          // pairs of 0x8000 | the largest scale that e serves (0 before the first)
+  __device__ __forceinline__ void init() {
+    held = 0;
+#pragma unroll
+    for (int i = 0; i < NG / 2; ++i) limit[i] = 0x80008000u;
+  }
+  __device__ __forceinline__ int e(int g) const { return (int)(held << (24 - 8 * g)) >> 24; }
+  __device__ __forceinline__ bool any() const { return held != 0; }
+  // Bits 15 and 31 are set where word w of a token's scales (word i: groups 2 i and 2 i + 1) is served. Words of
+  // tokens that do not exist hold anything: they may ask for a look at the scales, which skips them.
+  __device__ __forceinline__ uint32_t served(uint32_t w, int i) const { return limit[i % (NG / 2)] - w; }
+  // Larger of m and the word's finite scales: infinities and NaN set no power.
+  static __device__ __forceinline__ uint32_t larger(uint32_t m, uint32_t w) {
+    const uint32_t v = w & 0x7fff7fffu;
+    return __vmaxu2(m, v & ~__vcmpgtu2(v, 0x7bff7bffu));
+  }
+  // Takes the lanes' maxima m into the powers (the whole warp); f[g] is what group g's sums are to be
+  // multiplied by.
+  __device__ __forceinline__ void raise(uint32_t* m, float* f) {
+#pragma unroll
+    for (int i = 0; i < NG / 2; ++i)
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) m[i] = __vmaxu2(m[i], __shfl_xor_sync(0xffffffffu, m[i], x));
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int up = 16 * (g & 1), top = (int)(m[g >> 1] >> up & 0xffffu);
+      f[g] = 1.f;
+      if (top <= (int)(limit[g >> 1] >> up & 0x7fffu)) continue;
+      const int k = top >= 0x400 ? (top >> 10) - 15 : 7 - __clz(top);      // floor(log2)
+      const int to = k >= -8 && k <= 0 ? 0 : k > 0 ? k : max(k + 1, -15);
+      const int most = to < 15 ? ((to + 16) << 10) - 1 : 0x7bff;
+      f[g] = pow2i(e(g) - to);
+      held = (held & ~(0xffu << 8 * g)) | ((uint32_t)to & 0xffu) << 8 * g;
+      limit[g >> 1] = (limit[g >> 1] & (0xffff0000u >> up)) | (0x8000u | most) << up;
+    }
+  }
+};
+
 // ------------------------------------------------------------------------------------------------
 // A warp's stream of tokens
 // ------------------------------------------------------------------------------------------------

@@ -62,3 +62,39 @@ def test_scales_of_every_magnitude(C, bits):
     bad = np.flatnonzero((got != s[:, 0]).ravel())
     assert bad.size == 0, [(float(m[i] * 2.0 ** 25), float(got.ravel()[i]), float(s.ravel()[i])) for i in bad[:8]]
     np.testing.assert_array_equal(Q.unpack(ck.codes.cpu().numpy().reshape(-1, 64 * bits // 8)[:n], bits), c[:, 0])
+
+
+# ------------------------------------------------------------------------------------------------
+# Mapped product: the bound of fp32 sums, element by element
+# ------------------------------------------------------------------------------------------------
+
+def run_mapped(p, W, pool, scales, bits, table, lens, H_kv, d):
+    from cross_model_attention_map_b200.runner import QuantDecodeStep
+    st = QuantDecodeStep(len(lens), p.shape[1], W.shape[0], d, p.shape[2], H_kv=H_kv)
+    return st.run(torch.from_numpy(p).cuda(), torch.from_numpy(W).cuda(), cache(pool, scales, bits),
+                  i32(table), i32(lens)).cpu().numpy()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("H,H_kv,d", [(3, 3, 128), (6, 2, 64), (16, 2, 128)])
+@pytest.mark.parametrize("outlier,small", [(64.0, 1e-3), (3000.0, 1e-2), (6e4, 1e-2), (4e5, 1e-3)])
+@pytest.mark.parametrize("where", ["all"])
+def test_mapped_groups_of_different_size(C, bits, H, H_kv, d, outlier, small, where):
+    """One group of 32 elements is large; the others, which share
+    nothing with it, keep the precision that they have alone."""
+    rng = np.random.default_rng(81)
+    lens, page = [600, 70], 16
+    table, total = table_of(rng, lens, page)
+    rows = []
+    for n in lens:
+        x = rng.standard_normal((n, H_kv, d))
+        x[..., 32:64] *= small
+        x[..., 96:] *= 10 * small
+        at = slice(None) if where == "all" else slice(n // 2, n // 2 + 1)
+        x[at, :, :32] *= outlier
+        rows.append(x)
+    pool, scales = pool_with(rng, rows, table, total, page, bits)
+    p, W = mapped_inputs(rng, lens, 5, H, max(lens))
+    got = run_mapped(p, W, pool, scales, bits, table, lens, H_kv, d)
+    assert C.iamap_device_status() == 0
+    check_mapped(got, p, W, pool, scales, bits, table, lens, page)
