@@ -7,22 +7,23 @@
 // unit being a value head with up to eight of the receiver heads that read it, and each warp streams the
 // tokens of one unit with their weights through a ring of copies, 64 (or 32) at a time. No barrier stands
 // in the loop. Twelve ragged sequences of up to 32768 tokens, 14 rows to 64 heads over 8 value heads of 128
-// in 8 bits: 62 us, the weights 19 of them (weights formed by the CTA for its whole range, between barriers:
-// 104; by every warp for each step: 125). Four of 8704 tokens, 64 value heads in 4 bits: 56 us (62 with
+// in 8 bits: 64 us, the weights 19 of them (weights formed by the CTA for its whole range, between barriers:
+// 104; by every warp for each step: 125). Four of 8704 tokens, 64 value heads in 4 bits: 57 us (62 with
 // 32 tokens a step and three CTAs an SM).
 //
 // The product runs on matrix instructions with the codes as one operand (quant_tile.cuh). Its other
-// operand, the weight times the token's scale of the group, has to keep fp32's precision in fp16, so it
-// is held as two parts, high and low, in two columns of the same instruction:
+// operand, the weight times the token's scale of the group, has to keep fp32's precision in fp16, so the
+// product t is formed in fp32 and held as two parts, high and low, in two columns of their own sums:
 //
-//   w 2^k = h + l,  P1 = rn(h s),  P2 = rn(l s + (h s - P1))    (h s - P1 is exact in one fma)
+//   t = w 2^k (s 2^-e),  t = high + 2^-12 low,  error at most 2^-22 |t| or 2^-37
 //
-// which leaves an error of 2^-22 relative, or 2^-25 absolute: the first kernel brings the largest |w| of
-// each receiver and 512 tokens, which is what a range holds, into [2^13, 2^14), so the absolute part is far
-// below the largest products. The scales of a group are taken times a power of two where they are 2 and more
-// or small (ScalePowers). With one receiver a value head (group 1), the eight columns are the (group of 32,
-// part) pairs, and one operand serves all groups; otherwise they are (receiver, part) and the operand is
-// formed a group.
+// The first kernel brings the largest |w| of each receiver and 512 tokens, which is what a range holds, into
+// [2^13, 2^14), and ScalePowers a group's largest s into [1/2, 1): the absolute part is 2^-49 of the product
+// of the two, so a token that takes almost all of the weight, with values near zero, leaves the others their
+// bits. (Parts formed in fp16, from weights held in two, keep 2^-39 of it; 57 and 62 us where this takes 57
+// and 64.) With one receiver a value head (group 1), the eight columns are the (group of 32, part) pairs, and
+// one operand serves all groups; otherwise the operand is formed a group: up to four receivers with their
+// parts side by side, or eight with their parts in two tiles.
 //
 // Partial sums of the ranges go to the workspace; a third kernel adds them in a fixed order.
 #include <algorithm>
@@ -37,7 +38,7 @@ using namespace qt;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBlock = 32;           // tokens of one record of weights: RJ receivers' as (high, low) pairs
+constexpr int kBlock = 32;           // tokens of one record of weights, RJ receivers'
 // Tokens of a range. Four equal sequences of 8704 and twelve ragged ones of up to 32768: 56 and 62 us; with
 // ranges of 256 59 and 65, with 1024 55 and 98 (a ragged batch then has fewer ranges than the device CTAs).
 constexpr int kChunk = 512;
@@ -78,9 +79,9 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Weights of 32 tokens and one unit: of the tokens t and t + 4 the pair of high parts and the pair of low
-// parts, [4 groups of 8 tokens][RJ / 4][t = 0..3][receiver] for four and eight receivers, [4][t] for one:
-// the order in which a warp's lanes want them.
+// Weights of 32 tokens and one unit: of the tokens t and t + 4 a pair in fp32,
+// [4 groups of 8 tokens][RJ / 4][t = 0..3][receiver] for four and eight receivers, [4][t] for one: the order in
+// which a warp's lanes want them.
 //
 // The weights: a CTA a range of tokens for sixteen receivers, a warp 64 of the tokens. The products run on
 // matrix instructions with both factors in three bf16 parts, of 2^-8 and 2^-17 of the first at most; the six
@@ -217,23 +218,19 @@ __global__ void __launch_bounds__(kWeightThreads, 2) quant_weights_kernel(const 
       const float f0 = pow2i(power(8 * i + 2 * tid)), f1 = pow2i(power(8 * i + 2 * tid + 1));
       const int un = u0 + (8 * i + 2 * tid) / RJ;
       if (un >= p.units) continue;
-      uint32_t* rec = reinterpret_cast<uint32_t*>(p.records) +
+      float* rec = reinterpret_cast<float*>(p.records) +
                       (((int64_t)b * p.units + un) * n + block) * (RJ * kBlock) +
                       (RJ == 8 ? (tid >> 1) * 32 : 0) + (gid & 3) * (RJ == 1 ? 2 : 8) + (RJ == 1 ? 0 : (tid & 1) * 4);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const float* c = w[m][i];
-        const float x0 = c[0] * f0, y0 = c[2] * f0, x1 = c[1] * f1, y1 = c[3] * f1;
-        uint4 v;                                               // (high, low) of two receivers
-        v.x = pack_f16(x0, y0), v.z = pack_f16(x1, y1);
-        const float2 b0 = unpack_f16(v.x), b1 = unpack_f16(v.z);
-        v.y = pack_f16(x0 - b0.x, y0 - b0.y), v.w = pack_f16(x1 - b1.x, y1 - b1.y);
-        uint32_t* to = rec + (m >> 1) * (RJ * kBlock) + ((m & 1) * 2 + (gid >> 2)) * (RJ * 8);
+        const float4 v = make_float4(c[0] * f0, c[2] * f0, c[1] * f1, c[3] * f1);   // two receivers
+        float* to = rec + (m >> 1) * (RJ * kBlock) + ((m & 1) * 2 + (gid >> 2)) * (RJ * 8);
         if (RJ == 1) {
-          *reinterpret_cast<uint2*>(to) = make_uint2(v.x, v.y);
-          if (un + 1 < p.units) *reinterpret_cast<uint2*>(to + (int64_t)n * kBlock) = make_uint2(v.z, v.w);
+          *reinterpret_cast<float2*>(to) = make_float2(v.x, v.y);
+          if (un + 1 < p.units) *reinterpret_cast<float2*>(to + (int64_t)n * kBlock) = make_float2(v.z, v.w);
         } else {
-          *reinterpret_cast<uint4*>(to) = v;
+          *reinterpret_cast<float4*>(to) = v;
         }
       }
     }
@@ -292,10 +289,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
     for (int i = 0; i < 2 * NG; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[c][i][e] = 0.f;
-  // The operand of a column is rn(l' s + (h' s - rn(h' s))): a low column has h' = h, l' = l, a high one
-  // h' = 0, l' = h.
-  const bool lo = gid & 1;
-  const uint32_t own = lo ? 0xffffffffu : 0u;
+  const bool low = gid & 1;                                  // GM 0, 1: this column holds low parts
   ScalePowers<NG> pw;
   pw.init();
   uint32_t down[NG / 2];                                     // the groups' 2^-e; GM 0: all of this column's group
@@ -308,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
     const uint32_t* masks;
     if (!in.take(&st, &masks)) break;
     const uint32_t scales = st + TK * R;
-    const uint32_t weights = scales + TK * SB + (GM == 0 ? tid * 8 : tid * 32 + (gid >> 1) * 8);
+    const uint32_t weights = scales + TK * SB +
+                             (GM == 0 ? tid * 8 : tid * 32 + (GM == 1 ? gid >> 1 : (gid >> 2) * 16 + (gid & 3)) * 8);
     // a scale in the step that its group's power does not serve
     const uint2 all = lds64(scales + lane * 8 % (TK * SB));
     const uint2 all2 = TK * SB > 256 ? lds64(scales + 256 + lane * 8) : all;
@@ -323,15 +318,16 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
       }
       float f[NG];
       pw.raise(m, f);
+      if (GM == 0) {                                         // this lane's columns are group tid's
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+        for (int g = 1; g < NG; ++g) f[0] = tid == g ? f[g] : f[0];
+      }
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
+      for (int c = 0; c < CT; ++c)
 #pragma unroll
-          for (int k = 0; k < 2 * NG; ++k)                   // GM 0: this lane's columns are group tid's
+        for (int k = 0; k < 2 * NG; ++k)
 #pragma unroll
-            for (int z = 0; z < 4; ++z)
-              if (GM == 0 ? tid == g : k / 2 == g) o[c][k][z] *= f[g];
+          for (int z = 0; z < 4; ++z) o[c][k][z] *= f[GM == 0 ? 0 : k / 2];
       auto half = [&](int g) { return (uint32_t)__half_as_ushort(__float2half_rn(pow2i(-pw.e(g)))); };
 #pragma unroll
       for (int k = 0; k < NG / 2; ++k) {
@@ -342,7 +338,6 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
             if ((gid >> 1) % NG == g) down[k] = half(g) * 0x10001u;
       }
     }
-    const bool scaled = pw.any();
 #pragma unroll 1
     for (int h = 0; h < RB::kTiles / 2; ++h) {
       const uint32_t mask = masks[h];
@@ -352,65 +347,43 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
         ValueTile<D, BITS> vt;
         vt.load(st + tile * kTok * R);
         const uint32_t sp = scales + (tile * kTok + tid) * SB;           // tokens tid + 4 k
-        uint2 sc[4];
-        uint32_t sg[2];                                      // GM 0: this column's group's, as pairs
-        if (GM != 0) {
+        uint2 sc[4];                                         // GM 0: this column's group's scale alone
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sc[k] = lds_scales<NG>(sp + 4 * k * SB);
-        } else {
-          const uint32_t at = sp + 2 * ((gid >> 1) % NG);
+        for (int k = 0; k < 4; ++k)
+          sc[k] = GM != 0 ? lds_scales<NG>(sp + 4 * k * SB)
+                          : make_uint2(lds16(sp + 4 * k * SB + 2 * ((gid >> 1) % NG)), 0u);
+        float2 w[2];                                         // weights of tokens (tid, tid + 4), + 8
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            sg[k] = __byte_perm(lds16(at + 8 * k * SB), lds16(at + (8 * k + 4) * SB), 0x5410);
-        }
-        uint32_t hp[CT][2], lp[CT][2];                       // weight pairs, high and low parts
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint2 w = lds64(weights + h * REC + (GM == 0 ? (2 * q + k) * 32 : ((2 * q + k) * CT + c) * 128));
-            hp[c][k] = w.x & own, lp[c][k] = lo ? w.y : w.x;
-          }
-        if (scaled) {
-          if (GM == 0) {
-            sg[0] = hmul2(sg[0], down[0]), sg[1] = hmul2(sg[1], down[0]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              sc[k] = make_uint2(hmul2(sc[k].x, down[0]), NG == 4 ? hmul2(sc[k].y, down[NG / 2 - 1]) : 0u);
-          }
-        }
+        for (int k = 0; k < 2; ++k)
+          w[k] = lds<float2>(weights + h * REC + (2 * q + k) * (RJ * 32));
         if (mask != 0xffffffffu) {
           // tokens that do not exist: no weight and no scale (memory behind them may hold anything)
           const uint32_t m = mask >> (q * kTok + tid);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint32_t keep =
-                ((m >> (8 * k)) & 1 ? 0xffffu : 0u) | ((m >> (8 * k + 4)) & 1 ? 0xffff0000u : 0u);
-#pragma unroll
-            for (int c = 0; c < CT; ++c) hp[c][k] &= keep, lp[c][k] &= keep;
-            if (GM == 0) sg[k] &= keep;
-          }
-          if (GM != 0) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (!((m >> (4 * k)) & 1)) sc[k] = make_uint2(0, 0);
+            if (!((m >> (8 * k)) & 1)) w[k].x = 0.f, sc[2 * k] = make_uint2(0, 0);
+            if (!((m >> (8 * k + 4)) & 1)) w[k].y = 0.f, sc[2 * k + 1] = make_uint2(0, 0);
           }
         }
-        auto weight = [&](int c, int k, uint32_t s) {
-          const uint32_t minus = hmul2(hp[c][k] ^ 0x80008000u, s);
-          return hfma2(lp[c][k], s, hfma2(hp[c][k], s, minus));
-        };
+        // operands of group g: tokens (tid, tid + 4) and + 8; c = 1 the low parts (GM 2)
         uint32_t pb[CT][2];
-        if (GM == 0) pb[0][0] = weight(0, 0, sg[0]), pb[0][1] = weight(0, 1, sg[1]);
+        auto operands = [&](int g) {
+          const uint16_t f = (uint16_t)(down[(g >> 1) % (NG / 2)] >> 16 * (g & 1));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t s0 = g < 2 ? sc[2 * k].x : sc[2 * k].y, s1 = g < 2 ? sc[2 * k + 1].x : sc[2 * k + 1].y;
+            const uint64_t s = pair_f32(fma_f16((uint16_t)(s0 >> 16 * (g & 1)), f, 0.f),
+                                        fma_f16((uint16_t)(s1 >> 16 * (g & 1)), f, 0.f));
+            uint32_t hi, lo;
+            split_f16(mul2(pair_f32(w[k].x, w[k].y), s), hi, lo);
+            pb[0][k] = GM != 2 && low ? lo : hi;
+            if (GM == 2) pb[CT - 1][k] = lo;
+          }
+        };
+        if (GM == 0) operands(0);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          if (GM != 0) {
-#pragma unroll
-            for (int c = 0; c < CT; ++c)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) pb[c][k] = weight(c, k, scale_pair(sc + 2 * k, g));
-          }
+          if (GM != 0) operands(g);
           uint32_t r[4], t[4];
           vt.group(g, r, t);
 #pragma unroll
@@ -425,7 +398,8 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
   }
   if (!ALIGNED) cp_async_wait<0>();
 
-  // columns 2 tid, 2 tid + 1 are the two parts of receiver tid (GM 0: of group tid)
+  // columns 2 tid, 2 tid + 1 are the two parts of receiver tid (GM 0: of group tid), or of GM 2's two tiles the
+  // receivers 2 tid and 2 tid + 1
   const bool direct = ctx <= kChunk;
   float* o_s = reinterpret_cast<float*>(smem);               // [part][unit of the CTA][rj][D]
   if (p.parts > 1) __syncthreads();                          // the rings are free
@@ -436,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
   };
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
-    const int r = GM == 0 ? 0 : 4 * c + tid;
+    const int r = GM == 0 ? 0 : GM == 1 ? tid : 2 * tid + c;
     if (r >= nrj || !live) continue;
     const int power = j0 < j1 ? p.powers[(((int64_t)b * p.units + unit) * p.chunks + chunk) * RJ + r] : 0;
     float* dst = (p.parts > 1 ? o_s + ((part * p.hs + warp % p.hs) * p.rj + r) * D : row_of(unit, r)) +
@@ -446,11 +420,11 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
       if (GM == 0 && tid != g) continue;
       const int k = power - pw.e(g);
       const float dn0 = pow2i(-(k / 2)), dn1 = pow2i(-(k - k / 2));
-      const float* a = o[c][2 * g];
-      const float* d = o[c][2 * g + 1];
+      auto sum = [&](int i, int z) {                         // row z / 2 of the pair, both parts
+        return fmaf(GM == 2 ? o[CT - 1][i][z + c] : o[0][i][z + 1], kLow, o[0][i][GM == 2 ? z + c : z]) * dn0 * dn1;
+      };
       *reinterpret_cast<float4*>(dst + 32 * g) =
-          make_float4((a[0] + a[1]) * dn0 * dn1, (a[2] + a[3]) * dn0 * dn1, (d[0] + d[1]) * dn0 * dn1,
-                      (d[2] + d[3]) * dn0 * dn1);
+          make_float4(sum(2 * g, 0), sum(2 * g, 2), sum(2 * g + 1, 0), sum(2 * g + 1, 2));
     }
   }
   if (p.parts == 1) return;

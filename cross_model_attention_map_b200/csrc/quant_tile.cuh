@@ -284,6 +284,37 @@ __device__ __forceinline__ uint32_t scale_pair(const uint2* sc, int g) {
   return g < 2 ? __byte_perm(sc[0].x, sc[1].x, sel) : __byte_perm(sc[0].y, sc[1].y, sel);
 }
 
+// Two fp32 numbers in a register pair, and their products.
+__device__ __forceinline__ uint64_t pair_f32(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ float2 unpair_f32(uint64_t a) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// a * b + c of fp16 numbers a and b, in fp32.
+__device__ __forceinline__ float fma_f16(uint16_t a, uint16_t b, float c) {
+  float d;
+  asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(d) : "h"(a), "h"(b), "f"(c));
+  return d;
+}
+// A pair t of fp32 numbers as fp16 pairs: t = high + low 2^-12. A |t| under 2^15 leaves at most 2^3 to the low
+// part, and what is below fp16's range in the high one is not lost: the error is at most 2^-22 |t|, or 2^-37.
+constexpr float kLow = 1.f / 4096.f;
+__device__ __forceinline__ void split_f16(uint64_t t, uint32_t& high, uint32_t& low) {
+  const float2 x = unpair_f32(t), y = unpair_f32(mul2(t, pair_f32(4096.f, 4096.f)));
+  high = pack_f16(x.x, x.y);
+  low = pack_f16(fma_f16((uint16_t)high, 0xec00, y.x), fma_f16((uint16_t)(high >> 16), 0xec00, y.y));
+}
+
 // Exact 2^k for k in [-126, 127], clamped to it; larger shifts are made in two steps by the caller.
 __device__ __forceinline__ float pow2i(int k) {
   return __uint_as_float((uint32_t)(min(max(k, -126), 127) + 127) << 23);
@@ -291,8 +322,8 @@ __device__ __forceinline__ float pow2i(int k) {
 
 // A power of two for each group of a warp's value scales. The groups are elements that share nothing but
 // their tokens, so a large group may not cost a small one its bits: group g's scales are taken times 2^-e[g],
-// under 2. e is 0 as long as the group's largest scale so far lies in [2^-8, 2), and otherwise brings it to
-// [1, 2), or [1/2, 1) below that range. It only rises, so a group's sums are rescaled a few times at most.
+// under 2. e brings the group's largest scale so far to [1/2, 1) (beyond 2^15 and under 2^-16 as near as
+// fp16 has the power) and serves scales up to 4 times that, so a group's sums are rescaled a few times at most.
 template <int NG>
 struct ScalePowers {
   uint32_t held;                   // e[g] in byte g
@@ -303,7 +334,6 @@ struct ScalePowers {
     for (int i = 0; i < NG / 2; ++i) limit[i] = 0x80008000u;
   }
   __device__ __forceinline__ int e(int g) const { return (int)(held << (24 - 8 * g)) >> 24; }
-  __device__ __forceinline__ bool any() const { return held != 0; }
   // Bits 15 and 31 are set where word w of a token's scales (word i: groups 2 i and 2 i + 1) is served. Words of
   // tokens that do not exist hold anything: they may ask for a look at the scales, which skips them.
   __device__ __forceinline__ uint32_t served(uint32_t w, int i) const { return limit[i % (NG / 2)] - w; }
@@ -316,16 +346,12 @@ struct ScalePowers {
   // multiplied by.
   __device__ __forceinline__ void raise(uint32_t* m, float* f) {
 #pragma unroll
-    for (int i = 0; i < NG / 2; ++i)
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) m[i] = __vmaxu2(m[i], __shfl_xor_sync(0xffffffffu, m[i], x));
-#pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const int up = 16 * (g & 1), top = (int)(m[g >> 1] >> up & 0xffffu);
+      const int up = 16 * (g & 1), top = (int)__reduce_max_sync(0xffffffffu, m[g >> 1] >> up & 0xffffu);
       f[g] = 1.f;
       if (top <= (int)(limit[g >> 1] >> up & 0x7fffu)) continue;
       const int k = top >= 0x400 ? (top >> 10) - 15 : 7 - __clz(top);      // floor(log2)
-      const int to = k >= -8 && k <= 0 ? 0 : k > 0 ? k : max(k + 1, -15);
+      const int to = min(max(k + 1, -15), 15);
       const int most = to < 15 ? ((to + 16) << 10) - 1 : 0x7bff;
       f[g] = pow2i(e(g) - to);
       held = (held & ~(0xffu << 8 * g)) | ((uint32_t)to & 0xffu) << 8 * g;

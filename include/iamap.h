@@ -650,7 +650,10 @@ int iamap_sender_rows_quant(const void* q, const void* k_codes, const void* k_sc
  *   out[b, r, :] = sum_{j < ctx_lens[b]} (sum_s W[r, s] * p_rows[b, s, j]) * v[b, j, r / (H_r / H_kv), :]
  * p_rows fp32 [batch, H_s, ctx_stride] (entries at j >= ctx_lens[b] are not used), W fp32
  * [H_r, H_s], out fp32 [batch, H_r, d_v] (16-byte aligned). H_s, H_r <= 128; H_kv divides H_r.
- * Precision is that of fp32 sums; entries of p_rows or W beyond bf16's range (3.38e38) count as
+ * Precision is that of fp32 sums: w = sum_s W p and the sums over tokens are held in fp32, and a
+ * product of w and a scale enters with an error of at most 2^-22 of itself, or 2^-49 of the largest
+ * |w| of the receiver in a range of 512 tokens times the group's largest scale there (2^-41 where
+ * that scale is below 2^-16). Entries of p_rows or W beyond bf16's range (3.38e38) count as
  * infinite, and a sum that meets an infinity or NaN is not finite.
  * ws: iamap_mapped_av_paged_quant_workspace_bytes bytes (the weights, 4 bytes a token of max_ctx
  * and receiver head, and the partial sums of each 512 tokens).

@@ -78,9 +78,9 @@ def run_mapped(p, W, pool, scales, bits, table, lens, H_kv, d):
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("H,H_kv,d", [(3, 3, 128), (6, 2, 64), (16, 2, 128)])
 @pytest.mark.parametrize("outlier,small", [(64.0, 1e-3), (3000.0, 1e-2), (6e4, 1e-2), (4e5, 1e-3)])
-@pytest.mark.parametrize("where", ["all"])
+@pytest.mark.parametrize("where", ["all", "one"])
 def test_mapped_groups_of_different_size(C, bits, H, H_kv, d, outlier, small, where):
-    """One group of 32 elements is large; the others, which share
+    """One group of 32 elements is large, in every token or in one of them; the others, which share
     nothing with it, keep the precision that they have alone."""
     rng = np.random.default_rng(81)
     lens, page = [600, 70], 16
@@ -95,6 +95,55 @@ def test_mapped_groups_of_different_size(C, bits, H, H_kv, d, outlier, small, wh
         rows.append(x)
     pool, scales = pool_with(rng, rows, table, total, page, bits)
     p, W = mapped_inputs(rng, lens, 5, H, max(lens))
+    got = run_mapped(p, W, pool, scales, bits, table, lens, H_kv, d)
+    assert C.iamap_device_status() == 0
+    check_mapped(got, p, W, pool, scales, bits, table, lens, page)
+
+
+def heavy(rng, lens, S, rest):
+    """Rows of probabilities whose token 0 has all but `rest` of the mass."""
+    p, _ = mapped_inputs(rng, lens, S, 1, max(lens))
+    p = p.astype(np.float64)
+    p[:, :, 0] = 0
+    p *= rest / np.maximum(p.sum(-1, keepdims=True), 1e-30)
+    p[:, :, 0] = 1 - rest
+    return p.astype(np.float32)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("H,H_kv,d", [(3, 3, 128), (6, 2, 64), (16, 2, 128)])
+@pytest.mark.parametrize("rest", [1e-3, 1e-5, 1e-7])
+def test_mapped_beside_a_heavy_token(C, bits, H, H_kv, d, rest):
+    """A first token that takes almost all of the weight and whose values are zero: what the others add up to
+    keeps its precision."""
+    rng = np.random.default_rng(82)
+    lens, page = [2000, 40], 16
+    table, total = table_of(rng, lens, page)
+    rows = [rng.standard_normal((n, H_kv, d)) for n in lens]
+    for x in rows:
+        x[0] = 0
+    pool, scales = pool_with(rng, rows, table, total, page, bits)
+    p, W = heavy(rng, lens, 5, rest), rng.standard_normal((H, 5)).astype(np.float32)
+    got = run_mapped(p, W, pool, scales, bits, table, lens, H_kv, d)
+    assert C.iamap_device_status() == 0
+    check_mapped(got, p, W, pool, scales, bits, table, lens, page)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("H,H_kv,d", [(3, 3, 128), (6, 2, 64), (16, 2, 128)])
+@pytest.mark.parametrize("outlier,small", [(1.0, 1e-4), (6e4, 1e-3)])
+def test_mapped_small_groups_beside_a_heavy_token(C, bits, H, H_kv, d, outlier, small):
+    """Both at once: a token with almost all of the weight and no values, and small groups beside a large one."""
+    rng = np.random.default_rng(83)
+    lens, page = [1100, 40], 16
+    table, total = table_of(rng, lens, page)
+    rows = [rng.standard_normal((n, H_kv, d)) for n in lens]
+    for x in rows:
+        x[..., 32:] *= small
+        x[..., :32] *= outlier
+        x[0] = 0
+    pool, scales = pool_with(rng, rows, table, total, page, bits)
+    p, W = heavy(rng, lens, 5, 1e-5), rng.standard_normal((H, 5)).astype(np.float32)
     got = run_mapped(p, W, pool, scales, bits, table, lens, H_kv, d)
     assert C.iamap_device_status() == 0
     check_mapped(got, p, W, pool, scales, bits, table, lens, page)
