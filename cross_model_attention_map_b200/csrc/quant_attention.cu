@@ -14,8 +14,8 @@
 // exceeds it by more than 14 (then to 8 below the new maximum), which is rare after the first steps,
 // so most steps need no reduction across lanes and no rescaling. p and p s are fp16 (11 bits; the
 // output has 8): between 2^-24 and 2^15, with at least one p of the warp's tokens near 2^8 or above.
-// Scales of 2 and more could take p s beyond that: a step that holds one checks its products, and raises
-// the ref of a head whose products do. l = sum p is fp32.
+// A group's scales are taken times a power of two where they are 2 and more or small (ScalePowers), so p s
+// stays under 2^15. l = sum p is fp32.
 //
 // Ranges of one sequence are joined by a second kernel; a sequence that fits in one range is written by
 // the first. 48 sequences of 4587 to 16384 tokens, 64 heads on 8 of 128, all in 4 bits: 161 us, 3.6 TB/s of
@@ -105,6 +105,8 @@ __global__ void __launch_bounds__(kThreads, 4) quant_attention_kernel(const Attn
 #pragma unroll
     for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
   float ref[2] = {kNoRef, kNoRef}, l[2] = {0.f, 0.f};
+  ScalePowers<NG, false> pw;
+  pw.init();
   float most[2] = {kNoRef, kNoRef};                        // (ref + 14) / fq: the largest score that ref serves
   const int t0 = (gid >> 1) + 4 * (gid & 1);               // tokens of a tile in this lane's score rows: t0, t0 + 8
 
@@ -114,10 +116,23 @@ __global__ void __launch_bounds__(kThreads, 4) quant_attention_kernel(const Attn
     const uint32_t* masks;
     if (!in.take(&st, &masks)) break;
     const uint32_t vs = st + RB::K + RB::S;
-    // a scale of 2 or more, infinite or NaN among the step's values
-    const uint4 all = lds128(vs + RB::V + lane * 16 % RB::S);
-    const bool large = __any_sync(0xffffffffu, (all.x | all.y | all.z | all.w) & 0x40004000u);
     const uint32_t mask = masks[0];
+    // a scale among the step's values that its group's power does not serve
+    const uint4 all = lds128(vs + RB::V + lane * 16 % RB::S);
+    const uint32_t served = pw.served(all.x, 0) & pw.served(all.y, 1) & pw.served(all.z, 0) & pw.served(all.w, 1);
+    if (__any_sync(0xffffffffu, (served & 0x80008000u) != 0x80008000u)) {
+      uint32_t m[NG / 2] = {};
+      const uint32_t q[4] = {all.x, all.y, all.z, all.w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        if (mask >> (lane * 16 % RB::S + 4 * w) / SB & 1) m[w % (NG / 2)] = pw.larger(m[w % (NG / 2)], q[w]);
+      float f[NG];
+      pw.raise(m, f);
+#pragma unroll
+      for (int k = 0; k < 2 * NG; ++k)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[k][c] *= f[k / 2];
+    }
     // scores of two tiles, to be multiplied by fq: x[t][c], c = 0, 1 row gid, 2, 3 row gid + 8
     float x[2][4];
 #pragma unroll
@@ -140,9 +155,18 @@ __global__ void __launch_bounds__(kThreads, 4) quant_attention_kernel(const Attn
           if (!((mask >> (16 * t + tid + 4 * k)) & 1)) sc[t][k] = make_uint2(0, 0);
       }
     }
+    if (pw.any()) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          sc[t][k].x = hmul2(sc[t][k].x, pw.half(0) | pw.half(1) << 16);
+          if (NG == 4) sc[t][k].y = hmul2(sc[t][k].y, pw.half(NG - 2) | pw.half(NG - 1) << 16);
+        }
+    }
     const float m0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
     const float m1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-    const bool slow = __any_sync(0xffffffffu, m0 > most[0] || m1 > most[1] || large);
+    const bool slow = __any_sync(0xffffffffu, m0 > most[0] || m1 > most[1]);
     if (slow) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -164,60 +188,14 @@ __global__ void __launch_bounds__(kThreads, 4) quant_attention_kernel(const Attn
     // probabilities as the operand of the second product: pb[t][0] tokens (tid, tid + 4), [1] + 8
     uint32_t pb[2][2];
     float e[2][4];
-    auto probabilities = [&]() {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        pb[t][0] = movmatrix_trans(pack_f16(e[t][0], e[t][1]));
-        pb[t][1] = movmatrix_trans(pack_f16(e[t][2], e[t][3]));
-      }
-    };
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int c = 0; c < 4; ++c) e[t][c] = ex2(fmaf(x[t][c], fq[c & 1], -ref[c & 1]));
-    probabilities();
-    if (large) {
-      __half2 top = __float2half2_rn(0.f);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t w = hmul2(pb[t][k], scale_pair(sc[t] + 2 * k, g));
-            top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&w)));
-          }
-      if (__any_sync(0xffffffffu,
-                     __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f)))) {
-        // column gid's largest product, and the power of two that brings it under 2^14
-        float big = 0.f;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float2 a = unpack_f16(pb[t][k]), s = unpack_f16(scale_pair(sc[t] + 2 * k, g));
-              const float u = fabsf(a.x * s.x), v = fabsf(a.y * s.y);
-              big = fmaxf(big, fmaxf(u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f));
-            }
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        const int down = big > 32768.f ? (int)(__float_as_uint(big) >> 23) - 127 - 13 : 0;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int n = __shfl_sync(0xffffffffu, down, 8 * tid + 4 * c);
-          const float f = __uint_as_float((uint32_t)(127 - n) << 23);
-          ref[c] += (float)n;
-          if (n != 0) most[c] = (ref[c] + 14.f) / fq[c];
-          l[c] *= f;
-#pragma unroll
-          for (int k = 0; k < 2 * NG; ++k) o[k][c] *= f, o[k][c + 2] *= f;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) e[t][c] *= f, e[t][c + 2] *= f;
-        }
-        probabilities();
-      }
+    for (int t = 0; t < 2; ++t) {
+      pb[t][0] = movmatrix_trans(pack_f16(e[t][0], e[t][1]));
+      pb[t][1] = movmatrix_trans(pack_f16(e[t][2], e[t][3]));
     }
     l[0] += (e[0][0] + e[0][2]) + (e[1][0] + e[1][2]);
     l[1] += (e[0][1] + e[0][3]) + (e[1][1] + e[1][3]);
@@ -258,9 +236,11 @@ __global__ void __launch_bounds__(kThreads, 4) quant_attention_kernel(const Attn
     const float f = ex2(ref[c] - m);
     float* dst = o_s + (warp * kHeads + h) * D + 4 * gid;
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
+    for (int g = 0; g < NG; ++g) {
+      const float fg = f * pow2i(pw.e(g));
       *reinterpret_cast<float4*>(dst + 32 * g) =
-          make_float4(o[2 * g][c] * f, o[2 * g][c + 2] * f, o[2 * g + 1][c] * f, o[2 * g + 1][c + 2] * f);
+          make_float4(o[2 * g][c] * fg, o[2 * g][c + 2] * fg, o[2 * g + 1][c] * fg, o[2 * g + 1][c + 2] * fg);
+    }
   }
   __syncthreads();
   const int64_t unit = ((int64_t)b * p.k.H + hk) * p.htiles + ht;

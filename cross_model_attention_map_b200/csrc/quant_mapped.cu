@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[c][i][e] = 0.f;
   const bool low = gid & 1;                                  // GM 0, 1: this column holds low parts
-  ScalePowers<NG> pw;
+  ScalePowers<NG, true> pw;
   pw.init();
   uint32_t down[NG / 2];                                     // the groups' 2^-e; GM 0: all of this column's group
 #pragma unroll
@@ -328,14 +328,13 @@ __global__ void __launch_bounds__(kThreads, 2) quant_mapped_kernel(MappedParams 
         for (int k = 0; k < 2 * NG; ++k)
 #pragma unroll
           for (int z = 0; z < 4; ++z) o[c][k][z] *= f[GM == 0 ? 0 : k / 2];
-      auto half = [&](int g) { return (uint32_t)__half_as_ushort(__float2half_rn(pow2i(-pw.e(g)))); };
 #pragma unroll
       for (int k = 0; k < NG / 2; ++k) {
-        down[k] = half(2 * k) | half(2 * k + 1) << 16;
+        down[k] = pw.half(2 * k) | pw.half(2 * k + 1) << 16;
         if (GM == 0)
 #pragma unroll
           for (int g = 0; g < NG; ++g)
-            if ((gid >> 1) % NG == g) down[k] = half(g) * 0x10001u;
+            if ((gid >> 1) % NG == g) down[k] = pw.half(g) * 0x10001u;
       }
     }
 #pragma unroll 1

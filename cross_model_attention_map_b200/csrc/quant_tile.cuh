@@ -322,9 +322,11 @@ __device__ __forceinline__ float pow2i(int k) {
 
 // A power of two for each group of a warp's value scales. The groups are elements that share nothing but
 // their tokens, so a large group may not cost a small one its bits: group g's scales are taken times 2^-e[g],
-// under 2. e brings the group's largest scale so far to [1/2, 1) (beyond 2^15 and under 2^-16 as near as
-// fp16 has the power) and serves scales up to 4 times that, so a group's sums are rescaled a few times at most.
-template <int NG>
+// under 2. e serves the largest scale S so far and only rises, so a group's sums are rescaled a few times at
+// most. CLOSE: e brings S to [1/2, 1), beyond 2^15 and under 2^-16 as near as fp16 has the power, and serves
+// scales up to 4 S. Otherwise the same below 2^-8, 0 for S in [2^-8, 2), where nothing needs to be multiplied, and
+// above it S is brought to [1, 2).
+template <int NG, bool CLOSE>
 struct ScalePowers {
   uint32_t held;                   // e[g] in byte g
   uint32_t limit[NG / 2];          // pairs of 0x8000 | the largest scale that e serves (0 before the first)
@@ -334,6 +336,9 @@ struct ScalePowers {
     for (int i = 0; i < NG / 2; ++i) limit[i] = 0x80008000u;
   }
   __device__ __forceinline__ int e(int g) const { return (int)(held << (24 - 8 * g)) >> 24; }
+  __device__ __forceinline__ bool any() const { return held != 0; }
+  // 2^-e of group g in fp16, exact: e is in [-15, 15].
+  __device__ __forceinline__ uint32_t half(int g) const { return e(g) == 15 ? 0x200u : (uint32_t)(15 - e(g)) << 10; }
   // Bits 15 and 31 are set where word w of a token's scales (word i: groups 2 i and 2 i + 1) is served. Words of
   // tokens that do not exist hold anything: they may ask for a look at the scales, which skips them.
   __device__ __forceinline__ uint32_t served(uint32_t w, int i) const { return limit[i % (NG / 2)] - w; }
@@ -351,7 +356,7 @@ struct ScalePowers {
       f[g] = 1.f;
       if (top <= (int)(limit[g >> 1] >> up & 0x7fffu)) continue;
       const int k = top >= 0x400 ? (top >> 10) - 15 : 7 - __clz(top);      // floor(log2)
-      const int to = min(max(k + 1, -15), 15);
+      const int to = CLOSE || k < -8 ? min(max(k + 1, -15), 15) : max(k, 0);
       const int most = to < 15 ? ((to + 16) << 10) - 1 : 0x7bff;
       f[g] = pow2i(e(g) - to);
       held = (held & ~(0xffu << 8 * g)) | ((uint32_t)to & 0xffu) << 8 * g;

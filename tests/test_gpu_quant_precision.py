@@ -147,3 +147,66 @@ def test_mapped_small_groups_beside_a_heavy_token(C, bits, H, H_kv, d, outlier, 
     got = run_mapped(p, W, pool, scales, bits, table, lens, H_kv, d)
     assert C.iamap_device_status() == 0
     check_mapped(got, p, W, pool, scales, bits, table, lens, page)
+
+
+# ------------------------------------------------------------------------------------------------
+# Attention
+# ------------------------------------------------------------------------------------------------
+
+def check_weights(got, q, k, v, kb, vb, table, lens, page):
+    """The error of attention's output, group by group. The probability p' = 2^(x - ref) and the product
+    p' s / 2^E are rounded to fp16: by at most 2^-11 of themselves each (3 counted, for the exponential and the
+    sums), or by 2^-25 where they are subnormal. The largest p' of 32 tokens lies between 2^2 and 2^14, and at
+    2^11 or above in those that hold a sequence's largest score, so that 2^ref is at most 2^-2 of the 32 tokens'
+    largest probability, or 2^-11. 2^E is 1 where a group's largest scale S is in [2^-8, 2), and otherwise at
+    most 2 S; for S of 2 and more s / 2^E <= 2 may become subnormal and is rounded by 2^-25, which is
+    2^-24 S in each value at most."""
+    p, _ = Q.softmax_rows(q, *k, kb, table, lens, page, max(lens))
+    ref, mag = Q.weighted_values(p, *v, vb, table, lens, page)
+    st = score_tol(q, *k, kb, table, lens, page)[:, None, None]
+    tol = 2.0 ** -8 * np.abs(ref) + (2 * st + 3 * 2.0 ** -11) * mag
+    rep, qv = q.shape[1] // k[0].shape[1], Q.LEVELS[vb]
+    for b, n in enumerate(lens):
+        pos = np.arange(n)
+        s = v[1][table[b, pos // page], :, pos % page].astype(np.float64)
+        top = np.repeat(np.repeat(s.max(0), rep, axis=0), 32, axis=-1)
+        unit = np.where((top >= 2.0 ** -8) & (top < 2), 1.0, 2 * top)
+        tol[b] += np.where(top >= 2, 2.0 ** -24 * top * qv, 0.0)
+        for j in range(0, n, 32):
+            largest = p[b, :, j:j + 32].max(-1)
+            ulp = np.where(largest == p[b, :, :n].max(-1), 2.0 ** -11, 2.0 ** -2) * largest
+            tol[b] += min(32, n - j) * 2.0 ** -25 * qv * ulp[:, None] * (top + unit)
+    err = np.abs(got - ref)
+    assert (err <= tol).all(), (err / np.maximum(tol, 1e-300)).max()
+
+
+def run_attention(qb, k, v, kb, vb, table, lens):
+    from cross_model_attention_map_b200.runner import QuantAttention
+    a = QuantAttention(len(lens), qb.shape[1], qb.shape[2], max(lens), H_kv=k[0].shape[1])
+    return a.run(bf16(qb), cache(*k, kb), cache(*v, vb), i32(table), i32(lens)).float().cpu().numpy()
+
+
+@pytest.mark.parametrize("vb", [4, 8])
+@pytest.mark.parametrize("H,H_kv,d", [(4, 4, 128), (8, 1, 128), (6, 2, 64)])
+@pytest.mark.parametrize("outlier,small", [(1.0, 1e-6), (300.0, 1e-5), (6e4, 1e-4), (4e5, 1e-5)])
+@pytest.mark.parametrize("where", ["all", "one"])
+def test_attention_groups_of_different_size(C, vb, H, H_kv, d, outlier, small, where):
+    """One group large, in every token or in one, and the others small and the same in every token, so that
+    roundings do not cancel."""
+    rng = np.random.default_rng(91)
+    lens, page = [700, 45], 16
+    table, total = table_of(rng, lens, page)
+    one = np.abs(rng.standard_normal((1, H_kv, d)))
+    ks, vs = [], []
+    for n in lens:
+        ks.append(np.repeat(rng.standard_normal((1, H_kv, d)), n, axis=0))
+        x = np.repeat(one, n, axis=0)
+        x[..., 32:] *= small
+        x[slice(None) if where == "all" else slice(n - 1, n), :, :32] *= outlier
+        vs.append(x)
+    k = pool_with(rng, ks, table, total, page, 8)
+    v = pool_with(rng, vs, table, total, page, vb)
+    qb = bf16_bits(rng.standard_normal((2, H, d)).astype(np.float32))
+    got = run_attention(qb, k, v, 8, vb, table, lens)
+    assert C.iamap_device_status() == 0
+    check_weights(got, bf16_bits_to_f64(qb), k, v, 8, vb, table, lens, page)
