@@ -10,12 +10,14 @@
 //   S^T = K^ q^T (codes; group scales in fp32), x = S / sqrt(d) in base 2, p = 2^(x - ref),
 //   O^T += V^T (p s) with s the token's scale of the group.
 //
-// ref is a reference near the running maximum, not the maximum itself: it moves only when a score
-// exceeds it by more than 14 (then to 8 below the new maximum), which is rare after the first steps,
-// so most steps need no reduction across lanes and no rescaling. p and p s are fp16 (11 bits; the
-// output has 8): between 2^-24 and 2^15, with at least one p of the warp's tokens near 2^8 or above.
+// p and p s are fp16 (11 bits; the output has 8, and l = sum p is fp32), so their smallest step, 2^-24, has to be
+// small beside the probabilities that count. ref is an integer near the maximum of the step at hand: it moves
+// to 10 below that maximum, and only when the largest p leaves [2^2, 2^14], which is rare after the first
+// step, so most steps need no rescaling. It falls too: behind a token that takes almost all of the
+// weight, with values near zero, the others make up the output, and with a ref that only rises they are
+// rounded away (19 % off beside 0.9999; 164 us where this takes 165).
 // A group's scales are taken times a power of two where they are 2 and more or small (ScalePowers), so p s
-// stays under 2^15. l = sum p is fp32.
+// stays under 2^15.
 //
 // Ranges of one sequence are joined by a second kernel; a sequence that fits in one range is written by
 // the first. 48 sequences of 4587 to 16384 tokens, 64 heads on 8 of 128, all in 4 bits: 161 us, 3.6 TB/s of
@@ -36,6 +38,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kHeads = 8;            // query heads a CTA
 constexpr float kNoRef = -3e38f;
+// Base-2 logarithms of the largest p of a step: where a move of ref puts it, and the limits that bring one on.
+constexpr float kSet = 10.f, kMost = 14.f, kLeast = 2.f;
+constexpr float kFall = 48.f;        // ref stays this near its highest, so that rescaled sums fit fp32
 
 struct AttnParams {
   const __nv_bfloat16* q;
@@ -104,10 +109,9 @@ __global__ void __launch_bounds__(kThreads, 4) quant_attention_kernel(const Attn
   for (int i = 0; i < 2 * NG; ++i)
 #pragma unroll
     for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
-  float ref[2] = {kNoRef, kNoRef}, l[2] = {0.f, 0.f};
+  float ref[2] = {kNoRef, kNoRef}, highest[2] = {kNoRef, kNoRef}, l[2] = {0.f, 0.f};
   ScalePowers<NG, false> pw;
   pw.init();
-  float most[2] = {kNoRef, kNoRef};                        // (ref + 14) / fq: the largest score that ref serves
   const int t0 = (gid >> 1) + 4 * (gid & 1);               // tokens of a tile in this lane's score rows: t0, t0 + 8
 
   for (int i = 0; i < in.nsteps; ++i) {
@@ -166,18 +170,20 @@ __global__ void __launch_bounds__(kThreads, 4) quant_attention_kernel(const Attn
     }
     const float m0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
     const float m1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-    const bool slow = __any_sync(0xffffffffu, m0 > most[0] || m1 > most[1]);
-    if (slow) {
+    // a lane's own four tokens decide most steps: their largest p lies between the limits in every lane
+    const float y0 = fmaf(m0, fq[0], -ref[0]), y1 = fmaf(m1, fq[1], -ref[1]);
+    if (!__all_sync(0xffffffffu, y0 >= kLeast && y0 <= kMost && y1 >= kLeast && y1 <= kMost)) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         float m = c ? m1 : m0;
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        if (m > most[c]) {
-          const float r = fmaf(m, fq[c], -8.f), f = ex2(ref[c] - r);
+        const float y = fmaf(m, fq[c], -ref[c]);
+        if (m > -INFINITY && !(y >= kLeast && y <= kMost)) {
+          const float r = fmaxf(floorf(m * fq[c]) - kSet, highest[c] - kFall), f = ex2(ref[c] - r);
           ref[c] = r;
-          most[c] = (r + 14.f) / fq[c];
+          highest[c] = fmaxf(highest[c], r);
           l[c] *= f;
 #pragma unroll
           for (int k = 0; k < 2 * NG; ++k) o[k][c] *= f, o[k][c + 2] *= f;

@@ -157,8 +157,8 @@ def check_weights(got, q, k, v, kb, vb, table, lens, page):
     """The error of attention's output, group by group. The probability p' = 2^(x - ref) and the product
     p' s / 2^E are rounded to fp16: by at most 2^-11 of themselves each (3 counted, for the exponential and the
     sums), or by 2^-25 where they are subnormal. The largest p' of 32 tokens lies between 2^2 and 2^14, and at
-    2^11 or above in those that hold a sequence's largest score, so that 2^ref is at most 2^-2 of the 32 tokens'
-    largest probability, or 2^-11. 2^E is 1 where a group's largest scale S is in [2^-8, 2), and otherwise at
+    2^10 or above in those that hold a sequence's largest score, so that 2^ref is at most 2^-2 of the 32 tokens'
+    largest probability, or 2^-10. 2^E is 1 where a group's largest scale S is in [2^-8, 2), and otherwise at
     most 2 S; for S of 2 and more s / 2^E <= 2 may become subnormal and is rounded by 2^-25, which is
     2^-24 S in each value at most."""
     p, _ = Q.softmax_rows(q, *k, kb, table, lens, page, max(lens))
@@ -174,7 +174,7 @@ def check_weights(got, q, k, v, kb, vb, table, lens, page):
         tol[b] += np.where(top >= 2, 2.0 ** -24 * top * qv, 0.0)
         for j in range(0, n, 32):
             largest = p[b, :, j:j + 32].max(-1)
-            ulp = np.where(largest == p[b, :, :n].max(-1), 2.0 ** -11, 2.0 ** -2) * largest
+            ulp = np.where(largest == p[b, :, :n].max(-1), 2.0 ** -10, 2.0 ** -2) * largest
             tol[b] += min(32, n - j) * 2.0 ** -25 * qv * ulp[:, None] * (top + unit)
     err = np.abs(got - ref)
     assert (err <= tol).all(), (err / np.maximum(tol, 1e-300)).max()
@@ -210,3 +210,30 @@ def test_attention_groups_of_different_size(C, vb, H, H_kv, d, outlier, small, w
     got = run_attention(qb, k, v, 8, vb, table, lens)
     assert C.iamap_device_status() == 0
     check_weights(got, bf16_bits_to_f64(qb), k, v, 8, vb, table, lens, page)
+
+
+@pytest.mark.parametrize("vb,size", [(4, 1.0), (8, 1.0), (8, 0.1)])
+@pytest.mark.parametrize("H,H_kv,d", [(4, 4, 128), (8, 1, 128), (6, 2, 64)])
+@pytest.mark.parametrize("rest", [1e-3, 1e-4, 1e-6, 1e-12])
+@pytest.mark.parametrize("at", [0, 130])
+def test_attention_beside_a_heavy_token(C, vb, size, H, H_kv, d, rest, at):
+    """A token that takes all but `rest` of the mass and whose values are zero. The others have the same
+    probability and nearly the same values, so that roundings do not cancel."""
+    rng = np.random.default_rng(92)
+    lens, page, kb = [2048, 300], 16, 8
+    table, total = table_of(rng, lens, page)
+    dirs = rng.choice([-1.0, 1.0], size=(H_kv, d))             # |dir|^2 = d: a key t dir scores t sqrt(d) x
+    qb = bf16_bits(np.repeat(dirs, H // H_kv, axis=0)[None].repeat(2, 0).astype(np.float32))
+    ks, vs = [], []
+    for n in lens:
+        key = np.zeros((n, H_kv, d))
+        key[at] = dirs * math.log((n - 1) / rest) / math.sqrt(d)
+        ks.append(key)
+        x = np.abs(rng.standard_normal((1, H_kv, d))) * size * rng.uniform(0.9, 1.1, size=(n, 1, 1))
+        x[at] = 0
+        vs.append(x)
+    k = pool_with(rng, ks, table, total, page, kb)
+    v = pool_with(rng, vs, table, total, page, vb)
+    got = run_attention(qb, k, v, kb, vb, table, lens)
+    assert C.iamap_device_status() == 0
+    check_weights(got, bf16_bits_to_f64(qb), k, v, kb, vb, table, lens, page)
