@@ -142,9 +142,9 @@ __device__ __forceinline__ int q_elem(int p, int e) {
 }
 
 // The query operand of up to eight heads q[h * D], h < nh (the other columns are zero): head gid,
-// elements 8 tid .. 8 tid + 7 of every group. A head is brought near 2^7 by a power of two, so that bf16
-// values of any size are exact in fp16 (what is 2^-21 of the largest or less is rounded); fq[c] takes the
-// scores of columns 2 tid + c back, times `scale`.
+// elements 8 tid .. 8 tid + 7 of every group. A head's largest element is brought to [2^14, 2^15) by a
+// power of two, so that bf16 values of any size are exact in fp16 down to 2^-31 of it (less is rounded, by
+// at most 2^-39 of it); fq[c] takes the scores of columns 2 tid + c back, times `scale`.
 template <int D, int BITS>
 __device__ __forceinline__ void load_query(const __nv_bfloat16* q, int nh, float scale,
                                            uint32_t (*qf)[4], float* fq) {
@@ -163,7 +163,7 @@ __device__ __forceinline__ void load_query(const __nv_bfloat16* q, int nh, float
   }
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const int down = min(253, max(1, 261 - (int)(m >> 7)));          // exponent field of the power of two
+  const int down = min(253, max(1, 268 - (int)(m >> 7)));          // exponent field of the power of two
   const float f = __uint_as_float((uint32_t)down << 23);
   const float back = __uint_as_float((uint32_t)(254 - down) << 23) * scale;
 #pragma unroll

@@ -636,6 +636,9 @@ int iamap_cache_read(const void* codes, const void* scales, int64_t num_pages,
  *   p_rows  fp32 [batch, H_s, ctx_stride], ctx_stride >= max_ctx, written in full (zeros at
  *           j >= ctx_lens[b]; a sequence of length 0 has a row of zeros)
  *   ws      iamap_sender_rows_quant_workspace_bytes bytes
+ * Scores are fp32: the products of q and the codes are exact and summed 16 at a time, a group's sum is
+ * rounded once more as it is multiplied by its scale (here and in iamap_attention_paged_quant). Elements
+ * of q under 2^-31 of the head's largest are rounded, by at most 2^-39 of it.
  * The result feeds iamap_mapped_av_paged_quant (or iamap_mapped_av_paged) as its p_rows.
  */
 size_t iamap_sender_rows_quant_workspace_bytes(int batch, int H_s, int max_ctx);

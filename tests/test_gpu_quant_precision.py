@@ -153,7 +153,7 @@ def test_mapped_small_groups_beside_a_heavy_token(C, bits, H, H_kv, d, outlier, 
 # Attention
 # ------------------------------------------------------------------------------------------------
 
-def check_weights(got, q, k, v, kb, vb, table, lens, page):
+def check_weights(got, q, k, v, kb, vb, table, lens, page, off=0.0):
     """The error of attention's output, group by group. The probability p' = 2^(x - ref) and the product
     p' s / 2^E are rounded to fp16: by at most 2^-11 of themselves each (3 counted, for the exponential and the
     sums), or by 2^-25 where they are subnormal. The largest p' of 32 tokens lies between 2^2 and 2^14, and at
@@ -163,7 +163,7 @@ def check_weights(got, q, k, v, kb, vb, table, lens, page):
     2^-24 S in each value at most."""
     p, _ = Q.softmax_rows(q, *k, kb, table, lens, page, max(lens))
     ref, mag = Q.weighted_values(p, *v, vb, table, lens, page)
-    st = score_tol(q, *k, kb, table, lens, page)[:, None, None]
+    st = (score_tol(q, *k, kb, table, lens, page) + off)[:, None, None]
     tol = 2.0 ** -8 * np.abs(ref) + (2 * st + 3 * 2.0 ** -11) * mag
     rep, qv = q.shape[1] // k[0].shape[1], Q.LEVELS[vb]
     for b, n in enumerate(lens):
@@ -237,3 +237,40 @@ def test_attention_beside_a_heavy_token(C, vb, size, H, H_kv, d, rest, at):
     got = run_attention(qb, k, v, kb, vb, table, lens)
     assert C.iamap_device_status() == 0
     check_weights(got, bf16_bits_to_f64(qb), k, v, kb, vb, table, lens, page)
+
+
+# ------------------------------------------------------------------------------------------------
+# Queries
+# ------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_of_different_size(C, bits, d):
+    """A query's first 32 elements are 2^30 times the others and meet keys of zeros; the others make up the
+    scores. The query is held in fp16 with its largest element q_max in [2^14, 2^15): fp16's smallest step there
+    is 2^-24, so an element is off by at most 2^-25 / 2^14 = 2^-39 of q_max (an element above 2^-31 q_max, that is
+    2^-17, ends its 8 bits at 2^-24 and is exact), and a score by 2^-39 q_max sum |k| / sqrt(d). To first order a row is
+    off by twice that, relative, and attention's output by twice that times sum p |v|."""
+    from cross_model_attention_map_b200.runner import QuantSenderRows
+    rng = np.random.default_rng(95)
+    lens, H, H_k, page = [300, 33], 6, 2, 16
+    table, total = table_of(rng, lens, page)
+    ks = [rng.standard_normal((n, H_k, d)) for n in lens]
+    for x in ks:
+        x[..., :32] = 0
+    k = pool_with(rng, ks, table, total, page, bits)
+    q = rng.standard_normal((2, H, d))
+    q[..., :32] = 2.0 ** 30 * rng.uniform(1, 2, size=(2, H, 32))
+    qb = bf16_bits(q.astype(np.float32))
+    got = QuantSenderRows(2, H, d, max(lens), H_k=H_k).run(bf16(qb), cache(*k, bits), i32(table), i32(lens))
+    assert C.iamap_device_status() == 0
+    q = bf16_bits_to_f64(qb)
+    off = np.array([2.0 ** -39 * np.abs(q[b]).max() * np.abs(Q.sequence(*k, bits, table, b, n, page)[0]).sum(-1).max()
+                    / math.sqrt(d) for b, n in enumerate(lens)])
+    assert off.max() < 0.05                                   # first order will do
+    p, _ = Q.softmax_rows(q, *k, bits, table, lens, page, max(lens))
+    tol = 2 * (score_tol(q, *k, bits, table, lens, page) + off) + 2.0 ** -20
+    assert (np.abs(got.cpu().numpy() - p) <= tol[:, None, None] * p).all()
+    v = pool_with(rng, ks, table, total, page, bits)
+    out = run_attention(qb, k, v, bits, bits, table, lens)
+    check_weights(out, q, k, v, bits, bits, table, lens, page, off)
