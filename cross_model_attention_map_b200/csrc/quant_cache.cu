@@ -356,7 +356,7 @@ int check_quant_batch(const int32_t* ctx_lens, int max_ctx, int batch, int max_p
   if (batch < 1 || max_ctx < 0) return set_error(IAMAP_ERR_INVALID_ARG, "bad sizes");
   if ((int64_t)max_ctx > (int64_t)max_pages * page_size)
     return set_error(IAMAP_ERR_INVALID_ARG, "max_ctx=%d exceeds the page table", max_ctx);
-  if (max_ctx > 1 << 30) return set_error(IAMAP_ERR_UNSUPPORTED, "max_ctx must be at most 2^30");
+  if (max_ctx > kMaxCtx) return set_error(IAMAP_ERR_UNSUPPORTED, "max_ctx must be at most 2^30");
   return IAMAP_OK;
 }
 

@@ -24,6 +24,7 @@
 namespace iamap {
 
 constexpr int kQuantGroup = 32;
+constexpr int kMaxCtx = 1 << 30;     // longest max_ctx of the decode calls
 
 // The pages of one quantised cache and the page table that a call reads them through.
 struct QuantPages {

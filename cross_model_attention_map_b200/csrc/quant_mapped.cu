@@ -532,7 +532,7 @@ using namespace iamap;
 extern "C" size_t iamap_mapped_av_paged_quant_workspace_bytes(int batch, int H_r, int d_v,
                                                               int max_ctx) {
   if (batch < 1 || H_r < 1 || d_v < 1 || max_ctx < 0) return 0;
-  if (batch > 65535 || H_r > 128) return 0;                         // refused by the call
+  if (batch > 65535 || H_r > 128 || max_ctx > kMaxCtx) return 0;     // refused by the call
   // the most that any grouping of the H_r heads needs
   size_t most = 256;
   for (int group = 1; group <= H_r; ++group) {
@@ -570,13 +570,13 @@ extern "C" int iamap_mapped_av_paged_quant(const float* p_rows, int ctx_stride, 
   MappedParams p{};
   size_t powers_at = 0, partial_at = 0;
   const size_t need = mapped_shape(batch, H_kv, H_r / H_kv, d_v, max_ctx, &p, &powers_at, &partial_at);
+  const int64_t blocks = (int64_t)p.chunks * batch * p.slices;
+  if (blocks > 0x7fffffff)
+    return set_error(IAMAP_ERR_UNSUPPORTED, "batch times heads times max_ctx is too large");
   if (!ws || ws_bytes < need)
     return set_error(IAMAP_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws_bytes);
   if ((reinterpret_cast<uintptr_t>(ws) & 15u) != 0)
     return set_error(IAMAP_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
-  const int64_t blocks = (int64_t)p.chunks * batch * p.slices;
-  if (blocks > 0x7fffffff || p.chunks > 65535)
-    return set_error(IAMAP_ERR_UNSUPPORTED, "batch times heads times max_ctx is too large");
   DeviceContext* ctx = device_context();
   if (!ctx) return IAMAP_ERR_CUDA;
   p.rows = p_rows;

@@ -231,7 +231,7 @@ using namespace iamap;
 
 extern "C" size_t iamap_sender_rows_quant_workspace_bytes(int batch, int H_s, int max_ctx) {
   if (batch < 1 || H_s < 1 || max_ctx < 0) return 0;
-  if (batch > 65535 || (int64_t)batch * H_s > 0x7fffff) return 0;    // refused by the call
+  if (batch > 65535 || (int64_t)batch * H_s > 0x7fffff || max_ctx > kMaxCtx) return 0;   // refused by the call
   // the most that any grouping of the H_s heads needs
   size_t most = 256;
   for (int group = 1; group <= H_s; ++group) {

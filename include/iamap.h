@@ -597,8 +597,10 @@ int iamap_prefix_lookup(const uint64_t* keys, int64_t count, const int64_t* key_
  * A workspace (16-byte aligned) belongs to one call in flight: calls that may overlap on the GPU,
  * captured graphs among them, need one each; nothing in it is kept from one call for the next.
  * Limits (beyond them IAMAP_ERR_UNSUPPORTED): num_pages * H * page_size < 2^32, batch <= 65535,
- * batch times query heads < 2^23, max_ctx <= 2^30; the workspace queries return 0 for a batch beyond
- * them. Pages of a multiple of 16 tokens are read in whole tiles; any other page_size works, row by
+ * batch times query heads < 2^23, max_ctx <= 2^30; the workspace queries return 0 for a batch or a
+ * max_ctx beyond them. A grid holds less than 2^31 CTAs: sender rows take batch * H_s *
+ * ceil(ctx_stride / 4096) of them, the mapped step at most batch * H_r * ceil(max_ctx / 512).
+ * Pages of a multiple of 16 tokens are read in whole tiles; any other page_size works, row by
  * row and slower.
  * ------------------------------------------------------------------------------------------- */
 

@@ -437,6 +437,24 @@ def test_mapped_infinities_stay_in_their_head(C):
     assert torch.equal(got[0, [0, 2, 3]], clean[0, [0, 2, 3]])
 
 
+def test_mapped_with_room_for_a_very_long_context(C):
+    """max_ctx beyond 65535 ranges of 512 tokens, as a captured step that is to serve any length has it."""
+    from cross_model_attention_map_b200.runner import QuantDecodeStep
+    rng = np.random.default_rng(33)
+    lens, page, d, bits, most = [700, 30], 64, 64, 4, 33_600_000
+    table, total = table_of(rng, lens, page)
+    pool, scales = pool_of(rng, lens, table, total, page, 1, d, bits)
+    wide = torch.full((2, most // page), 1 << 30, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = i32(table)
+    p, W = mapped_inputs(rng, lens, 1, 1, 700)
+    rows = torch.zeros(2, 1, most, device="cuda")
+    rows[:, :, :700] = torch.from_numpy(p).cuda()
+    got = QuantDecodeStep(2, 1, 1, d, most).run(rows, torch.from_numpy(W).cuda(), cache(pool, scales, bits), wide,
+                                                i32(lens))
+    assert C.iamap_device_status() == 0
+    check_mapped(got.cpu().numpy(), p, W, pool, scales, bits, table, lens, page)
+
+
 # ------------------------------------------------------------------------------------------------
 # Attention
 # ------------------------------------------------------------------------------------------------

@@ -226,3 +226,21 @@ def test_batches_that_are_too_large(lib):
     assert lib.iamap_attention_paged_quant_workspace_bytes(65535, 1 << 30, 64, 20) == 0
     for call in (_rows, _mapped, _attend):
         assert call(lib, ws=A + 8) == INVALID and "16-byte" in lib.iamap_last_error()
+
+
+def test_contexts_that_are_too_long(lib):
+    """max_ctx is bounded alike in the calls and in their workspace queries; what the grid cannot hold is refused
+    whatever the workspace."""
+    long = dict(max_ctx=(1 << 30) + 1, max_pages=1 << 27, stride=2**31 - 1)
+    for call in (_rows, _mapped):
+        assert call(lib, **long) == UNSUPPORTED and "2^30" in lib.iamap_last_error()
+    del long["stride"]
+    assert _attend(lib, **long) == UNSUPPORTED and "2^30" in lib.iamap_last_error()
+    for n in ((1 << 30) + 1, 2**31 - 1):
+        assert lib.iamap_sender_rows_quant_workspace_bytes(1, 4, n) == 0
+        assert lib.iamap_mapped_av_paged_quant_workspace_bytes(1, 4, 64, n) == 0
+        assert lib.iamap_attention_paged_quant_workspace_bytes(1, 4, 64, n) == 0
+    assert lib.iamap_mapped_av_paged_quant_workspace_bytes(1, 4, 64, 1 << 30) > 0
+    at_most = dict(max_ctx=1 << 30, max_pages=1 << 27, stride=1 << 30, ws_bytes=0)
+    assert _mapped(lib, **at_most) == WORKSPACE
+    assert _mapped(lib, **at_most, batch=1024) == UNSUPPORTED and "too large" in lib.iamap_last_error()
