@@ -339,7 +339,8 @@ int check_quant_pages(const void* codes, const void* scales, int64_t num_pages,
   if (bits != 4 && bits != 8)
     return set_error(IAMAP_ERR_UNSUPPORTED, "a cache holds 4 or 8 bits an element, not %d", bits);
   if (d != 64 && d != 128) return set_error(IAMAP_ERR_UNSUPPORTED, "head dim must be 64 or 128");
-  if (!codes || !scales || !page_table) return set_error(IAMAP_ERR_INVALID_ARG, "null pointer");
+  // an empty page table has no address
+  if (!codes || !scales || (!page_table && max_pages != 0)) return set_error(IAMAP_ERR_INVALID_ARG, "null pointer");
   if (num_pages < 0 || max_pages < 0 || page_size < 1 || H < 1)
     return set_error(IAMAP_ERR_INVALID_ARG, "bad sizes of the cache");
   if (((reinterpret_cast<uintptr_t>(codes) | reinterpret_cast<uintptr_t>(scales)) & 15u) != 0)

@@ -586,6 +586,7 @@ int iamap_prefix_lookup(const uint64_t* keys, int64_t count, const int64_t* key_
  *   codes   uint8 [num_pages, H, page_size, d * bits / 8]   16-byte aligned
  *   scales  fp16  [num_pages, H, page_size, d / 32]         16-byte aligned
  * Token j of sequence b is slot j % page_size of page page_table[b * max_pages + j / page_size].
+ * With max_pages 0 (max_ctx 0: every sequence is empty) page_table may be NULL.
  * In a row, element 32 g + 4 r + i (r < 8, i < 4) is code number r * (d / 8) + 4 g + i, stored with
  * an offset: byte c + 128 (8 bits), or nibble c + 8, low nibble first (4 bits). Codes and scales
  * of slots at or past a sequence's length are never used (they may hold anything).

@@ -555,6 +555,28 @@ def test_bad_pages_are_absent_tokens(C, page):
     check_attention(out.float().cpu().numpy(), lse.cpu().numpy(), q, k, v, bits, bits, table, lens, page)
 
 
+def test_a_batch_of_empty_sequences(C):
+    """No sequence has a token, and the page table no column."""
+    from cross_model_attention_map_b200.runner import QuantAttention, QuantCache, QuantDecodeStep, QuantSenderRows
+    ck = QuantCache(2, 16, 2, 64, 4)
+    table, lens = torch.empty(3, 0, dtype=torch.int32, device="cuda"), i32([0, 0, 0])
+    q = torch.randn(3, 4, 64, device="cuda").bfloat16()
+    r = QuantSenderRows(3, 4, 64, 0, H_k=2, ctx_stride=5)
+    r.rows.fill_(float("nan"))
+    assert not r.run(q, ck, table, lens).any()
+    st = QuantDecodeStep(3, 4, 4, 64, 0, H_kv=2, ctx_stride=5)
+    st.out.fill_(float("nan"))
+    assert not st.run(r.rows, torch.randn(4, 4, device="cuda"), ck, table, lens).any()
+    a = QuantAttention(3, 4, 64, 0, H_kv=2, want_lse=True)
+    a.out.fill_(float("nan"))
+    out, lse = a.run(q, ck, ck, table, lens)
+    assert not out.any() and bool((lse == -math.inf).all())
+    none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    ck.write(none, i32([0, 0, 0, 0]), lens, table)
+    assert ck.read(i32([0, 0, 0, 0]), lens, table, none) is none
+    assert C.iamap_device_status() == 0
+
+
 # ------------------------------------------------------------------------------------------------
 # Together
 # ------------------------------------------------------------------------------------------------
