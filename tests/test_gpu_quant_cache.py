@@ -722,3 +722,67 @@ def test_chunked_prefill_over_a_quantised_cache(C):
     layer = ChunkPrefillLayer(starts, ends, H, d, 4, d, 0.95)
     got = layer.step(q, packed[0], W, packed[1])
     assert C.iamap_device_status() == 0 and bool(torch.isfinite(got).all()) and bool(got.any())
+
+
+def test_chunked_prefill_over_a_quantised_cache_matches_its_values(C):
+    """compress and mapped_av of a chunk whose keys and values were read back from quantised pages: the
+    float64 oracle of the chunk on the values that the pages stand for, and the bits of the same calls on
+    those values."""
+    import dataclasses
+
+    from cross_model_attention_map_b200.runner import ChunkPrefillLayer, QuantCache
+    from oracle import chunked as CH
+    from synth import chunk_of, make_prefill
+
+    from _gpu_common import check_output, gpu_kept
+    rng = np.random.default_rng(73)
+    H, H_r, d, page, starts, ends = 4, 6, 64, 16, [128, 0], [300, 90]
+    wl = make_prefill(ends, H_s=H, d=d, H_r=H_r, d_v=d, B=64, tau=0.9, seed=73)
+    cw = chunk_of(wl, starts, ends)
+    table, total = table_of(rng, ends, page)
+    read, stand = [], []
+    for x in (cw.k, cw.v):
+        ck = QuantCache(total, page, x.shape[1], d, 8)
+        ck.write(bf16(x), i32(cw.cu_k), i32([0, 0]), i32(table))
+        read.append(ck.read(i32(cw.cu_k), i32([0, 0]), i32(table),
+                            torch.empty(*x.shape, dtype=torch.bfloat16, device="cuda")))
+        c, s = Q.quantise(bf16_bits_to_f64(x), 8)
+        stand.append(bf16_bits((c * np.repeat(s.astype(np.float64), 32, axis=-1)).astype(np.float32)))
+    W = torch.from_numpy(wl.W).cuda()
+    outs, layers = [], []
+    for k, v in (read, [bf16(x) for x in stand]):
+        layers.append(ChunkPrefillLayer(starts, ends, H, d, H_r, d, wl.tau))
+        outs.append(layers[-1].step(bf16(cw.q), k, W, v))
+    torch.cuda.synchronize()
+    assert C.iamap_device_status() == 0
+    assert torch.equal(outs[0], outs[1])
+    ref = dataclasses.replace(cw, k=stand[0], v=stand[1])
+    check_output(outs[0].cpu().numpy(), CH.mapped_av_chunk(ref, gpu_kept(layers[0])))
+
+
+@pytest.mark.parametrize("H,H_kv", [(4, 4), (6, 2), (16, 2)])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_mapped_weights_that_are_not_finite(C, bits, H, H_kv, bad):
+    """An infinity or NaN in a row of W reaches that receiver alone, one in a row of probabilities inside the context
+    that sequence alone; the others are the same to the bit."""
+    from cross_model_attention_map_b200.runner import QuantDecodeStep
+    rng = np.random.default_rng(34)
+    lens, S, d, page = [100, 1, 1100], 3, 64, 16
+    table, total = table_of(rng, lens, page)
+    ck = cache(*pool_of(rng, lens, table, total, page, H_kv, d, bits), bits)
+    p, W = mapped_inputs(rng, lens, S, H, max(lens))
+    run = lambda p, W: QuantDecodeStep(3, S, H, d, max(lens), H_kv=H_kv).run(  # noqa: E731
+        torch.from_numpy(p).cuda(), torch.from_numpy(W).cuda(), ck, i32(table), i32(lens))
+    clean = run(p, W)
+    assert bool(torch.isfinite(clean).all())
+    W2 = W.copy()
+    W2[1, 2] = bad
+    got = run(p, W2)
+    rest = [r for r in range(H) if r != 1]
+    assert not torch.isfinite(got[:, 1]).any() and torch.equal(got[:, rest], clean[:, rest])
+    p2 = p.copy()
+    p2[2, 0, 700] = bad
+    got = run(p2, W)
+    assert not torch.isfinite(got[2]).any() and torch.equal(got[:2], clean[:2])
+    assert C.iamap_device_status() == 0
