@@ -1,6 +1,6 @@
 // iamap_sender_rows_quant: the small model's attention rows over a quantised key cache.
 //
-//   p[b, h, j] = 2^(x_j - lse2),  x_j = q[b, h] . k^[b, j, h / group] log2(e) / sqrt(d),  j < ctx[b]
+//   p[b, h, j] = 2^(x_j - ref) / z,  x_j = q[b, h] . k^[b, j, h / group] log2(e) / sqrt(d),  j < ctx[b]
 //
 // Bound by the key bytes (36 a token and head of 64 in 4 bits) and the rows written (4 bytes a token
 // and query head). The first kernel streams the keys as quant_attention.cu does, writes x in place of p
@@ -141,15 +141,15 @@ __global__ void __launch_bounds__(kThreads, 5) quant_rows_kernel(const RowsParam
     if (!p.single)
       p.ml[((int64_t)b * p.Hq + h0 + threadIdx.x) * p.splits + split] = make_float2(m, z);
     else
-      ml_s[0][threadIdx.x].x = z == 0.f ? INFINITY : m + log2f(z);
+      ml_s[0][threadIdx.x] = make_float2(m, z == 0.f ? 0.f : 1.f / z);
   }
   if (!p.single) return;
   __syncthreads();                                           // this CTA wrote all of its rows' scores
   for (int h = warp; h < nh; h += kWarps) {
     float* row = p.rows + ((int64_t)b * p.Hq + h0 + h) * p.stride;
-    const float lse = ml_s[0][h].x;
+    const float2 mi = ml_s[0][h];
     for (int j = lane; j < p.stride; j += 32)
-      row[j] = j < ctx && lse != INFINITY ? ex2(row[j] - lse) : 0.f;
+      row[j] = j < ctx && mi.y != 0.f ? ex2(row[j] - mi.x) * mi.y : 0.f;
   }
 }
 
@@ -169,28 +169,28 @@ __global__ void __launch_bounds__(kNormThreads) quant_rows_norm_kernel(RowsParam
   float x[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) x[k] = j0 + k * kNormThreads < ctx ? row[j0 + k * kNormThreads] : 0.f;
-  float lse = INFINITY;
+  float top = 0.f, inv = 0.f;
   if (part * kNormTokens < ctx) {
     const float2* ml = p.ml + r * p.splits;
     float m = kNoRef, z = 0.f;
     for (int s = lane; s < n; s += 32) {
       const float2 v = ml[s];
-      const float top = fmaxf(m, v.x);
-      z = z * ex2(m - top) + v.y * ex2(v.x - top);
-      m = top;
+      const float t = fmaxf(m, v.x);
+      z = z * ex2(m - t) + v.y * ex2(v.x - t);
+      m = t;
     }
-    float top = m;
+    top = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     z *= ex2(m - top);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    if (z != 0.f) lse = top + log2f(z);
+    if (z != 0.f) inv = 1.f / z;
   }
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int j = j0 + k * kNormThreads;
-    if (j < p.stride) row[j] = j < ctx && lse != INFINITY ? ex2(x[k] - lse) : 0.f;
+    if (j < p.stride) row[j] = j < ctx && inv != 0.f ? ex2(x[k] - top) * inv : 0.f;
   }
 }
 

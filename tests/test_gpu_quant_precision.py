@@ -274,3 +274,18 @@ def test_queries_of_different_size(C, bits, d):
     v = pool_with(rng, ks, table, total, page, bits)
     out = run_attention(qb, k, v, bits, bits, table, lens)
     check_weights(out, q, k, v, bits, bits, table, lens, page, off)
+
+
+@pytest.mark.parametrize("n,page", [(300, 16), (5000, 16), (600, 8)])
+def test_rows_of_equal_large_scores(C, n, page):
+    """n equal keys whose score is large: every probability is 1 / n to fp32's rounding (one exponential of 0, a sum
+    of n ones, a quotient and a product: 2^-22), however large the score."""
+    from cross_model_attention_map_b200.runner import QuantSenderRows
+    rng = np.random.default_rng(96)
+    table, total = table_of(rng, [n], page)
+    key = rng.choice([-1.0, 1.0], size=(1, 1, 64))
+    k = pool_with(rng, [np.repeat(7 * key, n, axis=0)], table, total, page, 4)
+    qb = bf16_bits((key * np.array([[[60.0], [61.0], [-59.0]]])).reshape(1, 3, 64).astype(np.float32))
+    got = QuantSenderRows(1, 3, 64, n, H_k=1).run(bf16(qb), cache(*k, 4), i32(table), i32([n])).cpu().numpy()
+    assert C.iamap_device_status() == 0
+    assert (np.abs(got * np.float64(n) - 1) <= 2.0 ** -22).all(), np.abs(got * n - 1).max()
