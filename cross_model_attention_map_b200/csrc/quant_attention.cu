@@ -20,10 +20,10 @@
 // stays under 2^15.
 //
 // Ranges of one sequence are joined by a second kernel; a sequence that fits in one range is written by
-// the first. 48 sequences of 4587 to 16384 tokens, 64 heads on 8 of 128, all in 4 bits: 161 us, 3.6 TB/s of
-// the cache; one of 131071, keys in 8 bits and values in 4: 47 us, 4.6 TB/s. What bounds it is turning codes
-// into fp16 operands: 64 % of the issue slots and 58 % of the integer pipe, which the matrix instructions'
-// issue takes from as well, with four warps a scheduler.
+// the first. 48 sequences of 4587 to 16384 tokens, 64 heads on 8 of 128, all in 4 bits: 165 us a pass, 3.5
+// TB/s of the cache; one of 131071, keys in 8 bits and values in 4: 51 us, 4.3 TB/s. What bounds it is turning
+// codes into fp16 operands: 63 % of the issue slots while an SM works and 58 % of the integer pipe, which the
+// matrix instructions' issue takes from as well, with four warps a scheduler.
 #include <algorithm>
 
 #include "internal.h"
@@ -327,12 +327,12 @@ __global__ void __launch_bounds__(T) quant_attention_join_kernel(AttnParams p) {
   if (p.lse && threadIdx.x == 0) p.lse[row] = z == 0.f ? -INFINITY : (m + log2f(z)) * kLn2;
 }
 
-// Ranges: enough CTAs to fill the device's 148 SMs four times over, at least 256 tokens and at most 2048
+// Ranges: enough CTAs to fill the device's SMs four times over, at least 256 tokens and at most 2048
 // each, so that one long sequence in a ragged batch is still spread; one range up to 512 tokens, which
 // saves the second kernel.
 void attention_split(int batch, int units, int max_ctx, int* chunk, int* splits) {
   const int64_t total = (int64_t)units * max_ctx;
-  int64_t c = (total + 148 * 4 - 1) / (148 * 4);
+  int64_t c = (total + kSms * 4 - 1) / (kSms * 4);
   c = (c + 255) / 256 * 256;
   *chunk = max_ctx <= 512 ? 512 : (int)std::min<int64_t>(2048, std::max<int64_t>(256, c));
   while ((max_ctx - 1) / *chunk >= 65535) *chunk *= 2;      // the grid's third dimension

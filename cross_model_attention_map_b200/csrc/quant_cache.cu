@@ -7,9 +7,9 @@
 // instructions for every 8 elements of 32 lanes, so: a lane holds half a group (the scale, its reciprocal
 // and the addresses serve 16 elements), a quotient is half of a paired fused multiply-add and addition, and
 // a CTA looks its tokens' places up once, while its loads are in flight. 40960 tokens of 40 heads of 128 in
-// 4 bits, written and read back: 195 us for 1.07 GB, 5.5 TB/s; the write is 102 of them, 3 in 4 issue slots
-// taken (rows not loaded ahead and single additions: 212; 8 elements a lane with IEEE divisions and a lookup
-// a lane: 693).
+// 4 bits, written and read back, a pass launched from Python: 207 us for 1.07 GB, 5.2 TB/s. Alone and cold the
+// write takes 103 us, with 3 in 4 issue slots taken, and the read 88 (rows not loaded ahead and single additions
+// made the pass 9 % longer; 8 elements a lane with IEEE divisions and a lookup a lane 3.5 times as long).
 #include <algorithm>
 
 #include "internal.h"
@@ -324,7 +324,7 @@ int cache_io_shape(int64_t n, int H, int d, CacheIoParams* p, unsigned int* bloc
   const int64_t per = (int64_t)H * (d / 16);
   if (per > 0x7fffffff / 2) return set_error(IAMAP_ERR_UNSUPPORTED, "too many heads");
   p->per = (int)per;
-  const int64_t most = std::min<int64_t>(kMaxTokens, 4096 / per), spread = (n + 148 * 6 - 1) / (148 * 6);
+  const int64_t most = std::min<int64_t>(kMaxTokens, 4096 / per), spread = (n + kSms * 6 - 1) / (kSms * 6);
   p->tokens = (int)std::max<int64_t>(1, std::min(most, spread));
   p->per_inv = (uint32_t)(((1ull << 32) + per - 1) / per);   // exact: used for numbers below 2^13 only
   *blocks = (unsigned int)((n + p->tokens - 1) / p->tokens);

@@ -25,6 +25,9 @@ namespace iamap {
 
 constexpr int kQuantGroup = 32;
 constexpr int kMaxCtx = 1 << 30;     // longest max_ctx of the decode calls
+// SMs that ranges are made for: a constant, because the workspace queries split without a device and the calls
+// have to split alike.
+constexpr int kSms = 148;
 
 // The pages of one quantised cache and the page table that a call reads them through.
 struct QuantPages {

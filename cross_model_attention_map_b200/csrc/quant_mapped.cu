@@ -7,7 +7,7 @@
 // unit being a value head with up to eight of the receiver heads that read it, and each warp streams the
 // tokens of one unit with their weights through a ring of copies, 64 (or 32) at a time. No barrier stands
 // in the loop. Twelve ragged sequences of up to 32768 tokens, 14 rows to 64 heads over 8 value heads of 128
-// in 8 bits: 64 us, the weights 19 of them (weights formed by the CTA for its whole range, between barriers:
+// in 8 bits: 64 us, the weights 18 of them (weights formed by the CTA for its whole range, between barriers:
 // 104; by every warp for each step: 125). Four of 8704 tokens, 64 value heads in 4 bits: 57 us (62 with
 // 32 tokens a step and three CTAs an SM).
 //
@@ -39,8 +39,8 @@ using namespace qt;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kBlock = 32;           // tokens of one record of weights, RJ receivers'
-// Tokens of a range. Four equal sequences of 8704 and twelve ragged ones of up to 32768: 56 and 62 us; with
-// ranges of 256 59 and 65, with 1024 55 and 98 (a ragged batch then has fewer ranges than the device CTAs).
+// Tokens of a range. Four equal sequences of 8704 and twelve ragged ones of up to 32768, before products were
+// formed in fp32: 56 and 62 us; with ranges of 256 59 and 65, with 1024 55 and 98 (a ragged batch then has fewer ranges than the device CTAs).
 constexpr int kChunk = 512;
 
 struct MappedParams {
@@ -495,7 +495,7 @@ int launch_weights(const MappedParams& p, cudaStream_t st) {
   constexpr int UN = kWeightSlots / RJ;
   const int slices = (p.units + UN - 1) / UN;
   const int64_t items = (int64_t)slices * p.batch * p.chunks;
-  quant_weights_kernel<RJ><<<(unsigned int)std::min<int64_t>(items, 148 * 2), kWeightThreads, 0, st>>>(p, slices);
+  quant_weights_kernel<RJ><<<(unsigned int)std::min<int64_t>(items, kSms * 2), kWeightThreads, 0, st>>>(p, slices);
   IAMAP_LAUNCH_CHECK("quant_weights_kernel");
   return IAMAP_OK;
 }

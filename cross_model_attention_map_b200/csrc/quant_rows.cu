@@ -6,8 +6,8 @@
 // and query head). The first kernel streams the keys as quant_attention.cu does, writes x in place of p
 // and the (reference, sum) of each range of tokens; the second joins a row's ranges in their order and
 // normalises its tokens, which are still in L2. Where max_ctx fits one range the first kernel does it all.
-// Four sequences of 8704 tokens, 14 heads of 64 in 4 bits: 14.4 us; sixteen of up to 32768, 14 heads on 2
-// key heads in 8 bits: 18.5 us. Both are mostly latency: the lengths, the page table, the codes and the join
+// Four sequences of 8704 tokens, 14 heads of 64 in 4 bits: 14.4 us a pass; sixteen of up to 32768, 14 heads
+// on 2 key heads in 8 bits: 20.5 us. Both are mostly latency: the lengths, the page table, the codes and the join
 // are read one after the other.
 #include <algorithm>
 
@@ -194,12 +194,12 @@ __global__ void __launch_bounds__(kNormThreads) quant_rows_norm_kernel(RowsParam
   }
 }
 
-// Ranges: twice as many CTAs as the 148 SMs hold at five each (sixteen ragged sequences: 20.5 us, 22.6 with
+// Ranges: twice as many CTAs as the SMs hold at five each (sixteen ragged sequences: 20.5 us, 22.6 with
 // half as many, while four equal ones take the same), 256 to 2048 tokens; one range up to 512 tokens, which
 // saves the second kernel.
 void rows_split(int units, int max_ctx, int* chunk, int* splits) {
   const int64_t total = (int64_t)units * max_ctx;
-  int64_t c = (total + 148 * 10 - 1) / (148 * 10);
+  int64_t c = (total + kSms * 10 - 1) / (kSms * 10);
   c = (c + 255) / 256 * 256;
   *chunk = max_ctx <= 512 ? 512 : (int)std::min<int64_t>(2048, std::max<int64_t>(256, c));
   while ((max_ctx - 1) / *chunk >= 65535) *chunk *= 2;      // the grid's third dimension

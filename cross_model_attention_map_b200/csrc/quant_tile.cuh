@@ -14,8 +14,9 @@
 //           elements) of four tokens; a byte permutation pairs two tokens, and the columns P carry the
 //           weight times the scale.
 //
-// Codes become fp16 exactly: 1024 + u is the fp16 number 0x6400 | u, from which 1024 + offset is taken
-// (for nibbles in the upper half of a byte 1024 + 16 u, one fused multiply-add).
+// Codes become fp16 exactly by the widely published conversion that writes a small integer into the
+// mantissa of a number whose last bit counts 1: 1024 + u is the fp16 number 0x6400 | u, from which
+// 1024 + offset is taken (for nibbles in the upper half of a byte 1024 + 16 u, one fused multiply-add).
 //
 // Row r of a 16-token tile is token (r & 8) + ((r & 7) >> 1) + 4 (r & 1): the two tokens of a pair of
 // columns 2 tid, 2 tid + 1 of P are then tokens tid and tid + 4 (+ 8), so that the lanes of one load of
