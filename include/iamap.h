@@ -678,8 +678,8 @@ int iamap_mapped_av_paged_quant(const float* p_rows, int ctx_stride, const float
  * j < ctx_lens[b] of q[b, h] . k[b, j, h / (H_q / H_kv)] / sqrt(d).
  *   q, out  bf16 [batch, H_q, d], 16-byte aligned. Scores, softmax statistics and sums are fp32. Each
  *           probability, and its product with a group's scale, is rounded to fp16: by 2^-11 of itself,
- *           or by 2^-27 of the largest probability among its 32 tokens (the product by 2^-19 of that
- *           times the group's largest scale) where that is more. Values whose scale is under 2^-15 of
+ *           or by 2^-27 of the largest probability among its 32 tokens (the product by 2^-18 of that
+ *           times the group's largest scale) where that is more. Values whose scale is under 2^-14 of
  *           the group's largest, where that is 2 or more, keep fewer bits. out is rounded to bf16 once.
  *   lse     fp32 [batch, H_q] natural-log sum of exp(scaled logits), or NULL
  * Keys and values lie in two pools with the same pages and page table, in k_bits and v_bits each.
