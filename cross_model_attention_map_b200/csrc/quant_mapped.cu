@@ -40,7 +40,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kBlock = 32;           // tokens of one record of weights, RJ receivers'
 // Tokens of a range. Four equal sequences of 8704 and twelve ragged ones of up to 32768, before products were
-// formed in fp32: 56 and 62 us; with ranges of 256 59 and 65, with 1024 55 and 98 (a ragged batch then has fewer ranges than the device CTAs).
+// formed in fp32: 56 and 62 us; with ranges of 256 59 and 65, with 1024 55 and 98 (a ragged batch then has
+// fewer ranges than the device CTAs).
 constexpr int kChunk = 512;
 
 struct MappedParams {

@@ -159,8 +159,8 @@ def check_weights(got, q, k, v, kb, vb, table, lens, page, off=0.0):
     sums), or by 2^-25 where they are subnormal. The largest p' of 32 tokens lies between 2^2 and 2^14, and at
     2^10 or above in those that hold a sequence's largest score, so that 2^ref is at most 2^-2 of the 32 tokens'
     largest probability, or 2^-10. 2^E is 1 where a group's largest scale S is in [2^-8, 2), and otherwise at
-    most 2 S, or 2^-15 (fp16 has no larger power of two than 2^15 to bring a scale up with); for S of 2 and more s / 2^E <= 2 may become subnormal and is rounded by 2^-25, which is
-    2^-24 S in each value at most."""
+    most 2 S, or 2^-15 (fp16 has no larger power of two than 2^15 to bring a scale up with). For S of 2 and
+    more s / 2^E <= 2 may become subnormal and is rounded by 2^-25, which is 2^-24 S in each value at most."""
     p, _ = Q.softmax_rows(q, *k, kb, table, lens, page, max(lens))
     ref, mag = Q.weighted_values(p, *v, vb, table, lens, page)
     st = (score_tol(q, *k, kb, table, lens, page) + off)[:, None, None]
